@@ -368,7 +368,7 @@ def _plain_policy(st, logp, old, adv, ref, mask, per_seq, clip_low, clip_high, d
         w = torch.where(total != 0, 1.0 / total, 0.0) * m
     else:
         n = _per_sequence(st, m)
-        w = (torch.where(n != 0, 1.0 / n, 0.0) / (n != 0).sum().clamp(min=1))[seq] * m
+        w = (torch.where(n != 0, 1.0 / n, 0.0) / n.numel())[seq] * m
     mean = lambda v: torch.where(m != 0, w * v, 0.0).sum(dtype=torch.float64).float()   # noqa: E731
     dlogp = torch.where(m != 0, w * (grad + kl_coef * dk), 0.0).float().reshape(logp.shape)
     return mean(token), mean(k), mean(clipped.double()), dlogp
@@ -478,12 +478,11 @@ def _exact_policy(logp, old, adv, ref, mask, bounds, per_seq, clip_low, clip_hig
     w, a = torch.zeros_like(m), torch.zeros_like(m)
     whole = m.sum()
     sums = [m[b:e].sum() for b, e in bounds]
-    full = max(1, sum(float(v) != 0 for v in sums))
     for s, (b, e) in enumerate(bounds):
         if reduce == "token":
             w[b:e] = m[b:e] / whole if float(whole) != 0 else 0.0
         elif float(sums[s]) != 0:
-            w[b:e] = m[b:e] / sums[s] / full
+            w[b:e] = m[b:e] / sums[s] / len(bounds)
         if per_seq:
             a[b:e] = adv[s].double()
     if not per_seq:
