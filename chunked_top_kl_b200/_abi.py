@@ -34,6 +34,10 @@ EXPORTS = (
     "kd_topk_kl_forward_backward_ex",
     "kd_teacher_topk_workspace_size",
     "kd_teacher_topk",
+    "kd_sequence_loss_workspace_size",
+    "kd_preference_loss",
+    "kd_policy_loss",
+    "kd_scale_gradient",
     "kd_selftest_wait_timeout",
 )
 
@@ -98,6 +102,17 @@ def load() -> ctypes.CDLL:
         lib.kd_teacher_topk_workspace_size.restype = sz
         lib.kd_teacher_topk.argtypes = [p, p, i64, i64, i64, i64, i64, p, p, p, sz, p]
         lib.kd_teacher_topk.restype = i32
+        f64 = ctypes.c_double
+        lib.kd_sequence_loss_workspace_size.argtypes = [i64]
+        lib.kd_sequence_loss_workspace_size.restype = sz
+        lib.kd_preference_loss.argtypes = [p, p, p, p, i32, i64, i64, f64, i32, f64, f64, i32, p, p, p, p, p,
+                                           p, sz, p]
+        lib.kd_preference_loss.restype = i32
+        lib.kd_policy_loss.argtypes = [p, p, p, p, i32, p, p, i32, i64, i64, f64, f64, f64, f64, i32, i32, p, p, p,
+                                       p, sz, p]
+        lib.kd_policy_loss.restype = i32
+        lib.kd_scale_gradient.argtypes = [p, p, p, i64, p]
+        lib.kd_scale_gradient.restype = i32
         lib.kd_selftest_wait_timeout.argtypes = [p, sz, i64, p]
         lib.kd_selftest_wait_timeout.restype = i32
         _lib = lib
@@ -213,6 +228,29 @@ def kd_teacher_topk_workspace_size(N: int, d: int, V: int, K: int, chunk: int) -
 def kd_teacher_topk(Ht, Wt, N, d, V, K, chunk, topk_idx, topk_logit, workspace, workspace_bytes, stream) -> int:
     return int(load().kd_teacher_topk(Ht, Wt, N, d, V, K, chunk, topk_idx, topk_logit, workspace,
                                       workspace_bytes, stream))
+
+
+def kd_sequence_loss_workspace_size(S: int) -> int:
+    return int(load().kd_sequence_loss_workspace_size(S))
+
+
+def kd_preference_loss(logp, ref_logp, mask, offsets, offsets_i64, S, N, beta, kind, label_smoothing, margin, average,
+                       grad_loss, loss, chosen, rejected, dlogp, workspace, workspace_bytes, stream) -> int:
+    return int(load().kd_preference_loss(logp, ref_logp, mask, offsets, offsets_i64, S, N, beta, kind,
+                                         label_smoothing, margin, average, grad_loss, loss, chosen, rejected, dlogp,
+                                         workspace, workspace_bytes, stream))
+
+
+def kd_policy_loss(logp, old_logp, ref_logp, advantages, advantages_per_sequence, mask, offsets, offsets_i64, S, N,
+                   clip_low, clip_high, dual_clip, kl_coef, kl_kind, per_sequence, grad_loss, loss, dlogp, workspace,
+                   workspace_bytes, stream) -> int:
+    return int(load().kd_policy_loss(logp, old_logp, ref_logp, advantages, advantages_per_sequence, mask, offsets,
+                                     offsets_i64, S, N, clip_low, clip_high, dual_clip, kl_coef, kl_kind,
+                                     per_sequence, grad_loss, loss, dlogp, workspace, workspace_bytes, stream))
+
+
+def kd_scale_gradient(x, g, out, N, stream) -> int:
+    return int(load().kd_scale_gradient(x, g, out, N, stream))
 
 
 def kd_selftest_wait_timeout(workspace, workspace_bytes, limit_us, stream) -> int:

@@ -1,0 +1,514 @@
+// Losses over token log-probabilities grouped into sequences: the preference
+// loss over paired sequences and the clipped policy loss with a KL term, each
+// with its gradient in the token log-probabilities.
+//
+// Both are bound by memory (a handful of operations per token and array), and
+// by launch latency below a few hundred thousand tokens.  Both are two
+// launches: the first sums what the second has to divide by or compare with
+// (a sequence's log ratio, the mask), the second reads the tokens, writes the
+// gradient and reduces the scalars.  The gradient thus comes with the loss,
+// in one reading of everything but the mask.
+//
+// Work is cut into items: a sequence, or one of `splits` ranges of it when the
+// sequences are few and long.  A team (a warp for short sequences, a block
+// otherwise) walks an item's tokens four at a time on 16-byte boundaries of
+// the arrays, so a sequence may begin and end anywhere.  Sums are kept in
+// 64 bits and joined in a fixed order: no result depends on the order in
+// which blocks run.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace kd {
+namespace seq {
+
+constexpr int kThreads = 256;
+constexpr int kSumBlocks = 592;      // blocks of the first launch at most (4 per SM): partial totals to join
+constexpr int kLossBlocks = 1184;    // blocks of the second launch at most (8 per SM)
+
+// The sequences of an array of N tokens: sequence s is [offsets[s],
+// offsets[s + 1]), or row s of S rows of L tokens when offsets is null.
+// Offsets are clamped to [0, N], so that no value of theirs leads outside
+// the arrays.
+struct Sequences {
+  const void* offsets;
+  int offsets_i64;
+  int64_t S, N, L;
+  int splits;          // items per sequence
+};
+
+__device__ __forceinline__ int64_t seq_offset(const Sequences& q, int64_t s) {
+  if (!q.offsets) return s * q.L;
+  int64_t o = q.offsets_i64 ? static_cast<const int64_t*>(q.offsets)[s]
+                            : (int64_t)static_cast<const int32_t*>(q.offsets)[s];
+  return o < 0 ? 0 : (o > q.N ? q.N : o);
+}
+
+// Tokens [lo, hi) of item k of sequence s.
+__device__ __forceinline__ void item_range(const Sequences& q, int64_t s, int k, int64_t& lo, int64_t& hi) {
+  const int64_t b = seq_offset(q, s), e = seq_offset(q, s + 1);
+  lo = b;
+  hi = e;
+  if (q.splits > 1) {
+    const int64_t a = b & ~int64_t(3);
+    const int64_t per = e > b ? ((e - a + q.splits - 1) / q.splits + 3) & ~int64_t(3) : 0;
+    const int64_t start = a + k * per;
+    if (start > lo) lo = start;
+    if (start + per < hi) hi = start + per;
+  }
+  if (hi < lo) hi = lo;
+}
+
+// Four tokens of an array from t0 (a multiple of 4): those of [lo, hi), zeros
+// for the others.
+template <bool VEC>
+__device__ __forceinline__ void load4(const float* __restrict__ p, int64_t t0, int64_t lo, int64_t hi, float (&v)[4]) {
+  if (VEC && t0 >= lo && t0 + 4 <= hi) {
+    const float4 f = *reinterpret_cast<const float4*>(p + t0);
+    v[0] = f.x;
+    v[1] = f.y;
+    v[2] = f.z;
+    v[3] = f.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = (t0 + j >= lo && t0 + j < hi) ? p[t0 + j] : 0.f;
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store4(float* __restrict__ p, int64_t t0, int64_t lo, int64_t hi, const float (&v)[4]) {
+  if (VEC && t0 >= lo && t0 + 4 <= hi) {
+    *reinterpret_cast<float4*>(p + t0) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (t0 + j >= lo && t0 + j < hi) p[t0 + j] = v[j];
+  }
+}
+
+// The four tokens' weights: the mask, or one, inside [lo, hi); 0 outside.
+template <bool VEC>
+__device__ __forceinline__ void load_mask4(const float* __restrict__ mask, int64_t t0, int64_t lo, int64_t hi,
+                                           float (&m)[4]) {
+  if (mask) {
+    load4<VEC>(mask, t0, lo, hi, m);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = (t0 + j >= lo && t0 + j < hi) ? 1.f : 0.f;
+  }
+}
+
+__device__ __forceinline__ double warp_sum64(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sum over a team, the same on every thread of it.  `red`: kThreads / 32
+// doubles of shared memory, free again when the call returns.
+template <int TEAM>
+__device__ __forceinline__ double team_sum(double v, double* red) {
+  v = warp_sum64(v);
+  if constexpr (TEAM > 32) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0;
+#pragma unroll
+    for (int w = 0; w < TEAM / 32; ++w) v += red[w];
+    __syncthreads();
+  }
+  return v;
+}
+
+// Sum of n values, by the lanes of one warp in a fixed order.
+__device__ __forceinline__ double warp_sum_array(const double* p, int64_t n, int stride) {
+  double v = 0.0;
+  for (int64_t i = threadIdx.x & 31; i < n; i += 32) v += p[i * stride];
+  return warp_sum64(v);
+}
+
+// The last block of a launch to get here (by `counter`, zeroed beforehand)
+// sums the blocks' partials in block order; every thread of it gets true.
+__device__ __forceinline__ bool last_block(unsigned int* counter) {
+  __shared__ bool last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(counter, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (last) __threadfence();
+  return last;
+}
+
+// Tokens in no sequence (before the first, behind the last) have no gradient.
+__device__ __forceinline__ void zero_outside(const Sequences& q, float* __restrict__ out) {
+  if (!q.offsets) return;
+  const int64_t b = seq_offset(q, 0), e = seq_offset(q, q.S);
+  const int64_t step = (int64_t)gridDim.x * blockDim.x, i0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  for (int64_t t = i0; t < b; t += step) out[t] = 0.f;
+  for (int64_t t = e + i0; t < q.N; t += step) out[t] = 0.f;
+}
+
+// ---------------------------------------------------------------- preference loss
+//
+// Sequences s and P + s (P = S / 2) are pair s's chosen and rejected answer.
+// With r_s = sum_t m_t (logp_t - ref_t), divided by sum_t m_t when averaged
+// (0 for a sequence without tokens),
+//   D = beta (r_s - r_{P+s}) - margin
+//   sigmoid: -(1 - e) log sigma(D) - e log sigma(-D)
+//   hinge:   max(0, 1 - D)
+//   ipo:     (r_s - r_{P+s} - margin - 1 / (2 beta))^2
+// the loss is the mean over the pairs and
+//   dlogp_t = +- g (dl/dD) (dD/dr) m_t / P  [/ sum m].
+// The difference of policy and reference is taken per token, so that the sum
+// holds the small log ratio and not two large log-probabilities.
+
+enum { kSigmoid = 0, kHinge = 1, kIpo = 2 };
+
+struct PrefArgs {
+  Sequences q;
+  const float *logp, *ref, *mask, *grad_loss;
+  double beta, smoothing, margin;
+  int kind, average;
+  double* sums;            // [S * splits][2]: sum m (logp - ref), sum m
+  double* part;            // [blocks] pair losses
+  unsigned int* counter;
+  float *loss, *chosen, *rejected, *dlogp;
+};
+
+template <int TEAM, bool VEC>
+__global__ void __launch_bounds__(kThreads) pref_sums_kernel(const PrefArgs A) {
+  __shared__ double red[kThreads / 32];
+  if (blockIdx.x == 0 && threadIdx.x == 0) *A.counter = 0u;
+  constexpr int kTeams = kThreads / TEAM;
+  const int tid = threadIdx.x % TEAM;
+  const int64_t items = A.q.S * A.q.splits;
+  for (int64_t it = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; it < items; it += (int64_t)gridDim.x * kTeams) {
+    const int64_t s = it / A.q.splits;
+    int64_t lo, hi;
+    item_range(A.q, s, (int)(it - s * A.q.splits), lo, hi);
+    double r = 0.0, n = 0.0;
+    for (int64_t t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM) {
+      float m[4], lp[4], rf[4] = {0.f, 0.f, 0.f, 0.f};
+      load_mask4<VEC>(A.mask, t0, lo, hi, m);
+      load4<VEC>(A.logp, t0, lo, hi, lp);
+      if (A.ref) load4<VEC>(A.ref, t0, lo, hi, rf);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (m[j] != 0.f) {                    // a masked place may hold anything, NaN included
+          r += (double)m[j] * ((double)lp[j] - (double)rf[j]);
+          n += (double)m[j];
+        }
+    }
+    r = team_sum<TEAM>(r, red);
+    n = team_sum<TEAM>(n, red);
+    if (tid == 0) {
+      A.sums[2 * it] = r;
+      A.sums[2 * it + 1] = n;
+    }
+  }
+}
+
+// Sequence s's log ratio and the factor of its tokens' weights (a whole warp calls).
+__device__ __forceinline__ void seq_ratio(const PrefArgs& A, int64_t s, double& r, double& w) {
+  const double* p = A.sums + 2 * s * A.q.splits;
+  r = warp_sum_array(p, A.q.splits, 2);
+  w = 1.0;
+  if (A.average) {
+    const double n = warp_sum_array(p + 1, A.q.splits, 2);
+    w = n != 0.0 ? 1.0 / n : 0.0;
+  }
+  r *= w;
+}
+
+__device__ __forceinline__ double softplus64(double v) { return (v > 0.0 ? v : 0.0) + log1p(exp(-fabs(v))); }
+
+template <int TEAM, bool VEC>
+__global__ void __launch_bounds__(kThreads) pref_loss_kernel(const PrefArgs A) {
+  __shared__ double red[kThreads / 32];
+  __shared__ float s_coef;
+  constexpr int kTeams = kThreads / TEAM;
+  const int tid = threadIdx.x % TEAM;
+  const int64_t items = A.q.S * A.q.splits, P = A.q.S / 2;
+  const double g = A.grad_loss ? (double)*A.grad_loss : 1.0;
+  double mine = 0.0;                          // pair losses of this thread's teams
+  for (int64_t it = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; it < items; it += (int64_t)gridDim.x * kTeams) {
+    const int64_t s = it / A.q.splits;
+    const int k = (int)(it - s * A.q.splits);
+    float coef = 0.f;
+    if (tid < 32) {
+      const bool is_chosen = s < P;
+      double r, w, ro, wo;
+      seq_ratio(A, s, r, w);
+      seq_ratio(A, is_chosen ? s + P : s - P, ro, wo);
+      const double diff = is_chosen ? r - ro : ro - r;
+      const double D = A.beta * diff - A.margin;
+      double l, slope;                        // the pair's loss and its derivative in r_chosen
+      if (A.kind == kSigmoid) {
+        l = (1.0 - A.smoothing) * softplus64(-D) + A.smoothing * softplus64(D);
+        slope = A.beta * (1.0 / (1.0 + exp(-D)) - (1.0 - A.smoothing));
+      } else if (A.kind == kHinge) {
+        l = D < 1.0 ? 1.0 - D : (D >= 1.0 ? 0.0 : D);        // NaN stays NaN
+        slope = D < 1.0 ? -A.beta : (D >= 1.0 ? 0.0 : D);
+      } else {
+        const double e = diff - A.margin - 0.5 / A.beta;
+        l = e * e;
+        slope = 2.0 * e;
+      }
+      coef = (float)((is_chosen ? slope : -slope) * w * g / (double)P);
+      if (tid == 0 && k == 0) {
+        if (is_chosen) {
+          mine += l;
+          A.chosen[s] = (float)(A.beta * r);
+        } else {
+          A.rejected[s - P] = (float)(A.beta * r);
+        }
+      }
+    }
+    if (!A.dlogp) continue;
+    if constexpr (TEAM > 32) {
+      if (threadIdx.x == 0) s_coef = coef;
+      __syncthreads();
+      coef = s_coef;
+      __syncthreads();
+    }
+    int64_t lo, hi;
+    item_range(A.q, s, k, lo, hi);
+    for (int64_t t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM) {
+      float m[4], d[4];
+      load_mask4<VEC>(A.mask, t0, lo, hi, m);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d[j] = m[j] != 0.f ? coef * m[j] : 0.f;
+      store4<VEC>(A.dlogp, t0, lo, hi, d);
+    }
+  }
+  if (A.dlogp) zero_outside(A.q, A.dlogp);
+  mine = team_sum<kThreads>(mine, red);
+  if (threadIdx.x == 0) A.part[blockIdx.x] = mine;
+  if (last_block(A.counter)) {
+    double v = 0.0;
+    for (unsigned i = threadIdx.x; i < gridDim.x; i += kThreads) v += __ldcg(A.part + i);
+    v = team_sum<kThreads>(v, red);
+    if (threadIdx.x == 0) *A.loss = P > 0 ? (float)(v / (double)P) : 0.f;
+  }
+}
+
+// ---------------------------------------------------------------- policy loss
+//
+// Per token, with x = logp - old, r = e^x and advantage A (the token's or its
+// sequence's):
+//   obj = min(r A, clip(r, 1 - lo, 1 + hi) A), and for A < 0 at least c A
+//         when a dual clip c is given
+//   kl  = y, y^2 / 2 or e^-y - 1 + y       (k1, k2, k3; y = logp - ref)
+//   l   = -obj + kl_coef kl
+// summed with weights w_t: m_t / sum m over all sequences, or m_t / (S sum of
+// the sequence's m), 0 where that sum is 0.  The gradient
+//   dlogp = g w ( [not clipped] (-A r) + kl_coef (1 | y | 1 - e^-y) )
+// treats old, ref and A as constants.
+//
+// Whether a token is clipped is decided in 64 bits, x against log(1 + hi),
+// log(1 - lo) and log c: a difference of two floats is exact there, so the
+// decision is that of the formula and not of a rounded exponential.  e^x and
+// the KL term are taken in 32 bits; e^-y - 1 + y, which cancels for small y,
+// by its series for |y| < 1/2.
+
+enum { kK1 = 0, kK2 = 1, kK3 = 2 };
+
+struct PolicyArgs {
+  Sequences q;
+  const float *logp, *old, *ref, *adv, *mask, *grad_loss;
+  int adv_per_seq, per_sequence, kl_kind, dual;
+  double log_hi, log_lo, log_dual;
+  float hi, lo, dual_c, kl_coef;
+  double* sums;            // [S * splits] sum m
+  double* total;           // [kSumBlocks] the first launch's blocks' sums
+  int sum_blocks;
+  double* part;            // [blocks][3]
+  unsigned int* counter;
+  float *loss, *dlogp;     // loss[3]: loss, KL, clipped share
+};
+
+template <int TEAM, bool VEC>
+__global__ void __launch_bounds__(kThreads) policy_sums_kernel(const PolicyArgs A) {
+  __shared__ double red[kThreads / 32];
+  if (blockIdx.x == 0 && threadIdx.x == 0) *A.counter = 0u;
+  constexpr int kTeams = kThreads / TEAM;
+  const int tid = threadIdx.x % TEAM;
+  const int64_t items = A.q.S * A.q.splits;
+  double all = 0.0;
+  for (int64_t it = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; it < items; it += (int64_t)gridDim.x * kTeams) {
+    const int64_t s = it / A.q.splits;
+    int64_t lo, hi;
+    item_range(A.q, s, (int)(it - s * A.q.splits), lo, hi);
+    double n = 0.0;
+    if (A.mask) {
+      for (int64_t t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM) {
+        float m[4];
+        load4<VEC>(A.mask, t0, lo, hi, m);
+        n += ((double)m[0] + (double)m[1]) + ((double)m[2] + (double)m[3]);
+      }
+      n = team_sum<TEAM>(n, red);
+    } else {
+      n = (double)(hi - lo);
+    }
+    if (tid == 0) {
+      A.sums[it] = n;
+      all += n;
+    }
+  }
+  all = team_sum<kThreads>(all, red);
+  if (threadIdx.x == 0) A.total[blockIdx.x] = all;
+}
+
+// (e^x - 1 - x) / x^2 for |x| < 1/2: sum_k x^k / (k + 2)!, k = 0..8 (the next term is below 2^-31 of it).
+__device__ __forceinline__ float exp_tail_series(float x) {
+  float p = 1.f / 3628800.f;
+  p = fmaf(p, x, 1.f / 362880.f);
+  p = fmaf(p, x, 1.f / 40320.f);
+  p = fmaf(p, x, 1.f / 5040.f);
+  p = fmaf(p, x, 1.f / 720.f);
+  p = fmaf(p, x, 1.f / 120.f);
+  p = fmaf(p, x, 1.f / 24.f);
+  p = fmaf(p, x, 1.f / 6.f);
+  return fmaf(p, x, 0.5f);
+}
+
+// One token: its loss, KL estimate, whether it is clipped, and d loss / d logp.
+__device__ __forceinline__ void policy_token(const PolicyArgs& A, float lp, float old, float ref, float a, float& loss,
+                                             float& kl, float& clipped, float& d) {
+  const double x = (double)lp - (double)old;
+  const float r = expf((float)x);
+  float obj = a == 0.f ? 0.f : r * a;         // A = 0: no term, whatever the ratio
+  float grad = -obj;
+  clipped = 0.f;
+  if (a > 0.f && x > A.log_hi) {
+    obj = (1.f + A.hi) * a;
+    grad = 0.f;
+    clipped = 1.f;
+  } else if (a < 0.f && x < A.log_lo) {
+    obj = (1.f - A.lo) * a;
+    grad = 0.f;
+    clipped = 1.f;
+  } else if (A.dual && a < 0.f && x > A.log_dual) {
+    obj = A.dual_c * a;
+    grad = 0.f;
+    clipped = 1.f;
+  }
+  kl = 0.f;
+  float dk = 0.f;
+  if (A.ref) {
+    const float y = lp - ref;
+    if (A.kl_kind == kK1) {
+      kl = y;
+      dk = 1.f;
+    } else if (A.kl_kind == kK2) {
+      kl = 0.5f * y * y;
+      dk = y;
+    } else if (fabsf(y) < 0.5f) {
+      kl = y * y * exp_tail_series(-y);       // e^-y - 1 + y
+      dk = y - kl;                            // 1 - e^-y
+    } else {
+      const float e = expf(-y);
+      kl = e - 1.f + y;
+      dk = 1.f - e;
+    }
+  }
+  loss = fmaf(A.kl_coef, kl, -obj);
+  d = fmaf(A.kl_coef, dk, grad);
+}
+
+template <int TEAM, bool VEC>
+__global__ void __launch_bounds__(kThreads) policy_loss_kernel(const PolicyArgs A) {
+  __shared__ double red[kThreads / 32];
+  constexpr int kTeams = kThreads / TEAM;
+  const int tid = threadIdx.x % TEAM;
+  const int64_t items = A.q.S * A.q.splits;
+  const float g = A.grad_loss ? *A.grad_loss : 1.f;
+  double inv_total = 0.0;
+  if (!A.per_sequence) {
+    double t = 0.0;
+    for (int i = threadIdx.x; i < A.sum_blocks; i += kThreads) t += A.total[i];
+    t = team_sum<kThreads>(t, red);
+    inv_total = t != 0.0 ? 1.0 / t : 0.0;
+  }
+  double sum_l = 0.0, sum_k = 0.0, sum_c = 0.0;
+  for (int64_t it = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; it < items; it += (int64_t)gridDim.x * kTeams) {
+    const int64_t s = it / A.q.splits;
+    int64_t lo, hi;
+    item_range(A.q, s, (int)(it - s * A.q.splits), lo, hi);
+    double w = inv_total;
+    if (A.per_sequence) {
+      const double n = warp_sum_array(A.sums + s * A.q.splits, A.q.splits, 1);   // every warp of the team
+      w = n != 0.0 ? 1.0 / (n * (double)A.q.S) : 0.0;
+    }
+    const float wg = (float)w * g;
+    const float as = A.adv_per_seq ? A.adv[s] : 0.f;
+    double il = 0.0, ik = 0.0, ic = 0.0;
+    for (int64_t t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM) {
+      float m[4], d[4] = {0.f, 0.f, 0.f, 0.f};
+      load_mask4<VEC>(A.mask, t0, lo, hi, m);
+      if (m[0] != 0.f || m[1] != 0.f || m[2] != 0.f || m[3] != 0.f) {
+        float lp[4], od[4], rf[4] = {0.f, 0.f, 0.f, 0.f}, a[4] = {as, as, as, as};
+        load4<VEC>(A.logp, t0, lo, hi, lp);
+        load4<VEC>(A.old, t0, lo, hi, od);
+        if (A.ref) load4<VEC>(A.ref, t0, lo, hi, rf);
+        if (!A.adv_per_seq) load4<VEC>(A.adv, t0, lo, hi, a);
+        float l4 = 0.f, k4 = 0.f, c4 = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (m[j] != 0.f) {                  // a masked place may hold anything, NaN included
+            float l, k, c, dd;
+            policy_token(A, lp[j], od[j], rf[j], a[j], l, k, c, dd);
+            l4 = fmaf(m[j], l, l4);
+            k4 = fmaf(m[j], k, k4);
+            c4 = fmaf(m[j], c, c4);
+            d[j] = wg * m[j] * dd;
+          }
+        il += (double)l4;
+        ik += (double)k4;
+        ic += (double)c4;
+      }
+      if (A.dlogp) store4<VEC>(A.dlogp, t0, lo, hi, d);
+    }
+    sum_l += w != 0.0 ? w * il : 0.0;
+    sum_k += w != 0.0 ? w * ik : 0.0;
+    sum_c += w != 0.0 ? w * ic : 0.0;
+  }
+  if (A.dlogp) zero_outside(A.q, A.dlogp);
+  sum_l = team_sum<kThreads>(sum_l, red);
+  sum_k = team_sum<kThreads>(sum_k, red);
+  sum_c = team_sum<kThreads>(sum_c, red);
+  if (threadIdx.x == 0) {
+    A.part[3 * blockIdx.x] = sum_l;
+    A.part[3 * blockIdx.x + 1] = sum_k;
+    A.part[3 * blockIdx.x + 2] = sum_c;
+  }
+  if (last_block(A.counter)) {
+    double v[3] = {0.0, 0.0, 0.0};
+    for (unsigned i = threadIdx.x; i < gridDim.x; i += kThreads)
+#pragma unroll
+      for (int j = 0; j < 3; ++j) v[j] += __ldcg(A.part + 3 * i + j);
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      v[j] = team_sum<kThreads>(v[j], red);
+      if (threadIdx.x == 0) A.loss[j] = (float)v[j];
+    }
+  }
+}
+
+// out = x g, the gradient of a loss whose unit gradient x was kept.
+template <bool VEC>
+__global__ void __launch_bounds__(kThreads) scale_kernel(const float* __restrict__ x, const float* __restrict__ g,
+                                                         float* __restrict__ out, int64_t n) {
+  const float s = *g;
+  for (int64_t t0 = 4 * ((int64_t)blockIdx.x * kThreads + threadIdx.x); t0 < n; t0 += 4 * (int64_t)gridDim.x * kThreads) {
+    float v[4];
+    load4<VEC>(x, t0, 0, n, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] *= s;
+    store4<VEC>(out, t0, 0, n, v);
+  }
+}
+
+}  // namespace seq
+}  // namespace kd

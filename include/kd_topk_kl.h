@@ -275,6 +275,67 @@ int kd_teacher_topk(const void* Ht, const void* Wt, int64_t N, int64_t d, int64_
                     int64_t chunk, int32_t* topk_idx, float* topk_logit,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Losses over token log-probabilities.  The arrays are fp32 [N], the tokens
+ * of S sequences: sequence s is [offsets[s], offsets[s + 1]) with offsets
+ * [S + 1] (int32, or int64 when offsets_i64 is 1) on the device, or, when
+ * offsets is NULL, row s of S rows of N / S tokens (N % S == 0).  Offsets are
+ * expected not to decrease; whatever their values, every access stays inside
+ * the arrays.  Tokens before offsets[0] or from offsets[S] on belong to no
+ * sequence.  mask is a weight per token, fp32 [N] or NULL (all ones); what the
+ * other arrays hold where it is 0 is not looked at (NaN included).  dlogp may
+ * be NULL (no gradient wanted); otherwise every element of it is written, 0
+ * for tokens that take no part.  grad_loss is a device fp32 scalar (the
+ * upstream gradient of the loss) or NULL for 1.0.  Arrays need 4-byte
+ * alignment (16-byte aligned ones are read faster), the workspace 256-byte.
+ * Sums are fp64 and in a fixed order: results are deterministic.  N < 2^40,
+ * S < 2^31.  The workspace's size goes by S alone. */
+size_t kd_sequence_loss_workspace_size(int64_t S);
+
+/* Preference loss over S / 2 pairs (S even): sequences s and S / 2 + s are a
+ * pair's chosen and rejected answer.  With r_s = sum_t m_t (logp_t - ref_t),
+ * divided by sum_t m_t when average is 1 (0 for a sequence whose weights sum
+ * to 0; ref_logp NULL: no reference, ref = 0), delta = r_s - r_{S/2+s} and
+ * D = beta delta - margin,
+ *   kind 0 (sigmoid): -(1 - label_smoothing) log sigma(D) - label_smoothing log sigma(-D)
+ *   kind 1 (hinge):   max(0, 1 - D)
+ *   kind 2 (ipo):     (delta - margin - 1 / (2 beta))^2
+ * (label_smoothing in [0, 1] enters kind 0 only).  Writes *loss, the mean
+ * over the pairs (0 for S = 0), the rewards beta r_s of the chosen and of the
+ * rejected sequences (fp32 [S / 2] each), and dlogp.  beta > 0. */
+int kd_preference_loss(const float* logp, const float* ref_logp, const float* mask,
+                       const void* offsets, int offsets_i64, int64_t S, int64_t N,
+                       double beta, int kind, double label_smoothing, double margin, int average,
+                       const float* grad_loss, float* loss, float* chosen, float* rejected, float* dlogp,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Clipped policy loss with a KL term.  Per token, with x = logp - old_logp,
+ * r = exp(x), advantage A (fp32, [N], or [S] with advantages_per_sequence = 1)
+ * and y = logp - ref_logp:
+ *   obj = min(r A, clip(r, 1 - clip_low, 1 + clip_high) A), and where A < 0 at
+ *         least dual_clip A (dual_clip > 1; 0 for none)
+ *   kl  = y | y^2 / 2 | exp(-y) - 1 + y        (kl_kind 0 | 1 | 2; 0 without ref_logp)
+ *   l   = -obj + kl_coef kl
+ * weighted by m_t / sum m over the tokens of all sequences, or, with
+ * per_sequence = 1, by m_t / (S sum of its sequence's m) (a sequence whose
+ * weights sum to 0 counts 0).  Writes loss[0] = sum w l, loss[1] = sum w kl,
+ * loss[2] = sum w [clipped], and dlogp = g w ([not clipped] (-A r) + kl_coef
+ * dkl/dlogp); old_logp, ref_logp and advantages are constants.  A token is
+ * clipped when A > 0 and x > log(1 + clip_high), A < 0 and
+ * x < log(1 - clip_low), or A < 0 and x > log(dual_clip); a token with A = 0
+ * has no first term.  0 <= clip_low < 1, clip_high >= 0. */
+int kd_policy_loss(const float* logp, const float* old_logp, const float* ref_logp,
+                   const float* advantages, int advantages_per_sequence, const float* mask,
+                   const void* offsets, int offsets_i64, int64_t S, int64_t N,
+                   double clip_low, double clip_high, double dual_clip, double kl_coef, int kl_kind,
+                   int per_sequence, const float* grad_loss, float* loss, float* dlogp,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* out[i] = x[i] * *g (fp32 [N]): the gradient of a loss whose unit gradient
+ * x one of the calls above has written, for an upstream gradient g on the
+ * device.  out may be x. */
+int kd_scale_gradient(const float* x, const float* g, float* out, int64_t N, void* stream);
+
 /* Failure-detection self-test.  Every pipeline wait in the kernels is
  * bounded: a barrier phase that does not complete within its limit makes the
  * waiting kernel record a timeout in the workspace's status words and exit,
