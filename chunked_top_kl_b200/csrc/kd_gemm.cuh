@@ -66,7 +66,8 @@ struct ProbArgs {
   int a_row0, b_row0;   // added to the row (M / N) coordinate
   int a_k0, b_k0;       // added to the K coordinate
   int dyn_role;         // with GemmArgs::dyn: the live rows are this GEMM's M (1: one tile per
-                        // unit, 3: band x column range units) or its K (2)
+                        // unit, 3 and 4: band x column range units, the schedule of 4, and with
+                        // DynRows::raster that of 3, read from device memory) or its K (2)
   int dyn_bands_fastest;
   int dyn_zero_fill;    // role 2 with no live rows: still write the (zero) output tiles
   int wide_cols;        // > 0: wide units (Prob WIDE): its 256-column tiles; the raster counts pairs of them
@@ -87,6 +88,9 @@ struct DynRows {
   const int* count;     // null: a static launch
   int row0;
   int chunk;
+  const Raster* raster; // roles 3 and 4: the schedule of the live rows (role 4) or of a chunk that
+                        // they fill in part (role 3), worked out by an earlier kernel; may be null
+                        // for role 3
 };
 
 // A launch runs problem 0 and, optionally, problem 1.  Problem 0's units go
@@ -120,11 +124,15 @@ __device__ __forceinline__ void wave_barrier(unsigned int* counter, unsigned int
 // The schedule of a launch with live row count `rows` (see DynRows).
 template <class G, bool HAS_P1>
 __device__ __forceinline__ void apply_live_rows(GemmArgs& a, int rows, int ngroups) {
+  const Raster* given = a.dyn.raster;
 #pragma unroll
   for (int p = 0; p < (HAS_P1 ? 2 : 1); ++p) {
     ProbArgs& pa = a.prob[p];
     if (pa.dyn_role == 1) {
       pa.raster = tile_raster(ceil_div64(rows, G::TILE_M), pa.raster.n_tiles, pa.dyn_bands_fastest != 0);
+    } else if (given && (pa.dyn_role == 3 || pa.dyn_role == 4)) {
+      if (rows == 0) pa.raster.num_units = 0;
+      else if (pa.dyn_role == 4 || rows != a.dyn.chunk) pa.raster = *given;
     } else if (pa.dyn_role == 3) {
       pa.raster = forward_raster(ceil_div64(rows, G::TILE_M), pa.raster.n_tiles, ngroups, 0, 0, kMaxDzSplits);
     } else if (pa.dyn_role == 2) {

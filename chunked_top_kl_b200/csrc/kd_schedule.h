@@ -86,7 +86,7 @@ KD_HD bool wide_pays(int64_t bands, int64_t n_cols, int64_t k0, int64_t U1, int6
 // go round-robin and the longer ranges (n_tiles % S of them, one tile
 // longer) come first in the unit order, so CTA 0 has both the most units,
 // w = ceil(m S / grid), and the most long ones, ceil(m (n_tiles % S) / grid)
-// at most: its load is w (n_tiles / S) + min(w, that).  (Exact for one band
+// at most: its load is w (n_tiles / S) + min(w, that) (split_cost).  (Exact for one band
 // group, and it picks the best S for the grouped forward rasters too.)
 //
 // The B operand (the vocabulary rows) is the large one, so a wave should
@@ -94,21 +94,19 @@ KD_HD bool wide_pays(int64_t bands, int64_t n_cols, int64_t k0, int64_t U1, int6
 // the same ranges side by side, group_m = grid / 2 (two ranges per wave),
 // capped so the group's A bands (band_bytes each, kept in L2) take at most
 // half of `l2_budget`, and evened out over the groups.
-KD_HD Raster forward_raster(int64_t m_tiles, int64_t n_tiles, int grid, int64_t band_bytes = 0,
-                            int64_t l2_budget = 0, int max_splits = kMaxSplits) {
-  int best_s = 1;
-  int64_t best_cost = (int64_t)1 << 62;
-  for (int s = 1; s <= max_splits && s <= n_tiles; ++s) {
-    const int64_t w = ceil_div64(m_tiles * s, grid);
-    const int64_t longs = ceil_div64(m_tiles * (n_tiles % s), grid);
-    const int64_t cost = w * (n_tiles / s) + (longs < w ? longs : w);
-    if (cost < best_cost) { best_cost = cost; best_s = s; }
-  }
+KD_HD int64_t split_cost(int64_t m_tiles, int64_t n_tiles, int grid, int s) {
+  const int64_t w = ceil_div64(m_tiles * s, grid);
+  const int64_t longs = ceil_div64(m_tiles * (n_tiles % s), grid);
+  return w * (n_tiles / s) + (longs < w ? longs : w);
+}
+
+KD_HD Raster split_raster(int64_t m_tiles, int64_t n_tiles, int grid, int splits, int64_t band_bytes,
+                          int64_t l2_budget) {
   Raster r;
   r.m_tiles = (int)m_tiles;
   r.n_tiles = (int)n_tiles;
-  r.splits = best_s;
-  r.tiles_per_split = (int)ceil_div64(n_tiles, best_s);
+  r.splits = splits;
+  r.tiles_per_split = (int)ceil_div64(n_tiles, splits);
   int64_t gm = grid / 2;
   if (band_bytes > 0 && l2_budget > 0) {
     const int64_t cap = l2_budget / 2 / band_bytes;
@@ -121,6 +119,30 @@ KD_HD Raster forward_raster(int64_t m_tiles, int64_t n_tiles, int grid, int64_t 
   r.num_units = (int)(m_tiles * r.splits);
   return r;
 }
+
+KD_HD Raster forward_raster(int64_t m_tiles, int64_t n_tiles, int grid, int64_t band_bytes = 0,
+                            int64_t l2_budget = 0, int max_splits = kMaxSplits) {
+  int best_s = 1;
+  int64_t best_cost = (int64_t)1 << 62;
+  for (int s = 1; s <= max_splits && s <= n_tiles; ++s) {
+    const int64_t cost = split_cost(m_tiles, n_tiles, grid, s);
+    if (cost < best_cost) { best_cost = cost; best_s = s; }
+  }
+  return split_raster(m_tiles, n_tiles, grid, best_s, band_bytes, l2_budget);
+}
+
+// Label log-probabilities: column ranges of one band at most, enough to occupy
+// every CTA pair with a single band of rows.
+constexpr int kLogpMaxSplits = 96;
+
+// Partial slots (one per row and column range) for N tokens: 16 ranges of
+// every row, as the distillation forward has, and 96 for up to one band of
+// rows, so that few live rows can be cut finer.
+KD_HD int64_t logp_part_slots(int64_t N) { return 16 * N + (int64_t)kLogpMaxSplits * 256; }
+
+// Units of a forward schedule over at most N rows (see forward_raster and the
+// slots above): 96 for one band, else ceil(rows / 256) * slots / rows.
+KD_HD int64_t logp_units_bound(int64_t N) { return kLogpMaxSplits + logp_part_slots(N) / 128; }
 
 // Two problems in one launch.  Problem 0's U0 units (k0 K blocks each) go
 // round-robin over `groups`, so groups [0, r), r = U0 % groups, run one more

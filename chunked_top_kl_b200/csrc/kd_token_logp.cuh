@@ -1,0 +1,424 @@
+// Label log-probabilities of tokens under the LM head, and their gradient:
+//   z = H W^T / T,  lse_n = log sum_v exp z_nv,  logp_n = z[n, y_n] - lse_n,
+//   ent_n = lse_n - sum_v p_nv z_nv              (p = softmax z)
+//   dZ_nv = (1/T) [ g_n (1[v = y_n] - p_nv) - h_n p_nv (log p_nv + ent_n) ]
+//   dH = dZ W,  dW = dZ^T H
+// for upstream gradients g of logp and h of ent.
+//
+// The products are the GEMM of kd_gemm.cuh with the epilogues below; as in
+// the distillation loss the logits are never stored, and recomputed chunk by
+// chunk for the gradient.  Both passes are bound by the tensor cores once
+// there are a few hundred tokens, by the bytes of W below that (2 V d read).
+//
+// Only tokens that count are multiplied: a negative label (a prompt token) and,
+// going back, a token whose upstream gradient is zero (masked or clipped) have
+// their rows left out.  The rows that stay are listed on the device, their H
+// rows gathered (N d 4 bytes of copying against 2 N d V operations), and the
+// GEMMs take the row count and the schedule for it from device memory.
+#pragma once
+
+#include "kd_gemm.cuh"
+
+namespace kd {
+
+constexpr int kLabelThreads = 1024;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// What the label scan leaves for the kernels behind it.
+struct LiveRows {
+  int count;         // rows that take part
+  int pad;
+  Raster raster;     // forward: of all of them; backward: of the last, partly filled chunk
+};
+
+struct LabelPrep {
+  const void* labels;
+  int labels_i64;
+  int N, V;
+  const float *dlogp, *dent;      // backward: upstream gradients (dent may be null); null in the forward pass
+  float *logp, *lse, *ent;        // forward: outputs to clear for tokens that take no part (ent may be null)
+  int32_t *rowmap, *lab;          // the live tokens in order, and their labels
+  LiveRows* live;
+  Status* status;
+  // the schedule: rows of `chunk` at most (backward; 0: all rows), column tiles, CTA pairs
+  int64_t chunk;
+  int n_tiles, groups, max_splits;
+  int64_t part_slots;             // forward: bounds the ranges by the partial slots (0: no bound)
+  int64_t band_bytes, l2_bytes;
+  unsigned int* wave;             // forward: pacing counters to clear
+};
+
+// One block lists the tokens that take part, in increasing order, with their
+// labels.  Labels at or above V are counted in the status words; their
+// log-probability is NaN, and they take no further part.
+__global__ void __launch_bounds__(kLabelThreads) label_prep_kernel(const LabelPrep P) {
+  __shared__ int s_warp[kLabelThreads / 32];
+  __shared__ unsigned int s_bad;
+  __shared__ unsigned long long s_best;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  if (t == 0) {
+    s_bad = 0u;
+    s_best = ~0ull;
+  }
+  int total = 0;
+  for (int64_t base = 0; base < P.N; base += 4 * kLabelThreads) {
+    const int64_t n0 = base + 4 * t;
+    int lab[4], keep = 0;
+    unsigned int bad = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      lab[j] = -1;
+      const int64_t n = n0 + j;
+      if (n >= P.N) continue;
+      const int64_t y = P.labels_i64 ? static_cast<const int64_t*>(P.labels)[n]
+                                     : (int64_t)static_cast<const int32_t*>(P.labels)[n];
+      bool on = y >= 0 && y < P.V;
+      const bool wrong = y >= P.V;
+      bad += wrong;
+      if (P.dlogp) {
+        on = on && (P.dlogp[n] != 0.f || (P.dent && P.dent[n] != 0.f));    // NaN stays in
+      } else if (!on) {
+        const float v = wrong ? __int_as_float(0x7fc00000) : 0.f;
+        P.logp[n] = v;
+        P.lse[n] = v;
+        if (P.ent) P.ent[n] = v;
+      }
+      if (on) {
+        lab[j] = (int)y;
+        ++keep;
+      }
+    }
+    int scan = keep;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += v;
+    }
+    __syncthreads();                       // the last tile's totals have been read
+    if (lane == 31) s_warp[warp] = scan;
+    if (bad) atomicAdd(&s_bad, bad);
+    __syncthreads();
+    int w = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += v;
+    }
+    const int before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+    int o = total + (warp > 0 ? before : 0) + scan - keep;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (lab[j] >= 0) {
+        P.rowmap[o] = (int32_t)(n0 + j);
+        P.lab[o++] = lab[j];
+      }
+    total += __shfl_sync(0xffffffffu, w, 31);
+  }
+  // The schedule of the live rows: forward_raster's search, a thread for each number of ranges.
+  const int64_t rows = P.chunk > 0 ? total % P.chunk : total;
+  const int64_t m_tiles = ceil_div64(rows, 256);
+  int64_t most = P.max_splits;
+  if (P.part_slots > 0 && rows > 0 && P.part_slots / rows < most) most = P.part_slots / rows;
+  __syncthreads();
+  if (rows > 0 && t + 1 <= most && t + 1 <= P.n_tiles)
+    atomicMin(&s_best, ((unsigned long long)split_cost(m_tiles, P.n_tiles, P.groups, t + 1) << 32) | (unsigned)(t + 1));
+  __syncthreads();
+  Raster r{};
+  if (rows > 0)
+    r = split_raster(m_tiles, P.n_tiles, P.groups, (int)(unsigned)s_best, P.band_bytes, P.l2_bytes);
+  if (t == 0) {
+    P.live->count = total;
+    P.live->raster = r;
+    P.status->bad_index = s_bad;
+    P.status->timeout = 0u;
+  }
+  if (P.wave)
+    for (int64_t i = t; i < wave_slots_bound(r.num_units, 0); i += kLabelThreads) P.wave[i] = 0u;
+}
+
+// Rows [row0, row0 + C) of the live list: dst[r] = src[rowmap[row0 + r]]
+// (16-byte vectors, d8 per row), a warp per row.  Rows past the live ones are
+// zero up to the end of the last band of 256, as far as the GEMMs read.
+__global__ void __launch_bounds__(256)
+gather_live_kernel(const uint4* __restrict__ src, int d8, const int32_t* __restrict__ rowmap,
+                   const LiveRows* __restrict__ live, int row0, int C, uint4* __restrict__ dst) {
+  int rows = live->count - row0;
+  rows = rows < 0 ? 0 : (rows > C ? C : rows);
+  const int64_t end = ceil_div64(rows, 256) * 256 < C ? ceil_div64(rows, 256) * 256 : C;
+  for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < end; r += (int64_t)gridDim.x * 8) {
+    const uint4* from = r < rows ? src + (size_t)rowmap[row0 + r] * d8 : nullptr;
+    for (int j = threadIdx.x & 31; j < d8; j += 32)
+      dst[(size_t)r * d8 + j] = from ? from[j] : make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// Forward: running scaled maximum and sum-exp over the unit's vocabulary
+// columns, the label's logit, and with ENT the sum of e u that the entropy
+// needs.  In log2 units, u_v = z_v zl2 - mb with zl2 = log2(e) / T and
+// mb = max z * zl2 as rounded: s = sum 2^u and t = sum 2^u u (u <= 0, so t
+// does not cancel).  A new maximum shifts u by delta = mb_old - mb_new:
+// t <- 2^delta (t + delta s), s <- 2^delta s.  Partials (mb, s, t, label
+// logit) per live row and column range; columns >= V are taken as -1e30.
+template <bool ENT>
+struct EpiLogp {
+  static constexpr bool kStaging = false;
+  struct Params {
+    int V;
+    float zl2;
+    const int32_t* lab;
+    float *part_m, *part_s, *part_t, *part_g;
+  };
+  float mrun, srun, trun, grun;
+  int grow, rows, label;
+
+  __device__ __forceinline__ void begin_unit(const Params& P, int grow_, int, int, const EpiCtx& cx) {
+    grow = grow_;
+    rows = cx.rows_valid;
+    mrun = -INFINITY;
+    srun = 0.f;
+    trun = 0.f;
+    grun = 0.f;
+    label = grow < rows ? P.lab[grow] : -1;
+  }
+
+  __device__ __forceinline__ void tile(const Params& P, const CUtensorMap*, int, int n, uint32_t taddr, EpiCtx&) {
+    const float zl2 = P.zl2;
+#pragma unroll 1
+    for (int j = 0; j < BN / 64; ++j) {
+      float v[64];
+      __syncwarp();
+      tmem_ld_32x32b_x64(taddr + j * 64, v);
+      const int c0 = n * BN + j * 64;
+      if (c0 + 64 > P.V) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (c0 + i >= P.V) v[i] = -1e30f;
+      }
+      if (label >= c0 && label < c0 + 64) grun = pick64(v, label - c0);     // once per row
+      float t[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) t[i] = fmaxf(v[i], v[i + 32]);
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1)
+#pragma unroll
+        for (int i = 0; i < w; ++i) t[i] = fmaxf(t[i], t[i + w]);
+      const float mn = fmaxf(mrun, t[0]);
+      const float mb = mn * zl2;
+      if (mn > mrun) {                        // rare after the first columns
+        const float delta = mrun * zl2 - mb;
+        const float f = ex2_approx(delta);
+        if (ENT) trun = f > 0.f ? f * fmaf(delta, srun, trun) : 0.f;
+        srun *= f;
+        mrun = mn;
+      }
+      const float2 zl2v = make_float2(zl2, zl2), nmb = make_float2(-mb, -mb);
+      float2 a01 = make_float2(0.f, 0.f), a23 = a01, b01 = a01, b23 = a01;
+#pragma unroll
+      for (int i = 0; i < 64; i += 4) {
+        const float2 u01 = __ffma2_rn(make_float2(v[i + 0], v[i + 1]), zl2v, nmb);
+        const float2 u23 = __ffma2_rn(make_float2(v[i + 2], v[i + 3]), zl2v, nmb);
+        const float2 e01 = make_float2(ex2_approx(u01.x), ex2_approx(u01.y));
+        const float2 e23 = make_float2(ex2_approx(u23.x), ex2_approx(u23.y));
+        a01 = __fadd2_rn(a01, e01);
+        a23 = __fadd2_rn(a23, e23);
+        if (ENT) {
+          b01 = __ffma2_rn(e01, u01, b01);
+          b23 = __ffma2_rn(e23, u23, b23);
+        }
+      }
+      srun += (a01.x + a01.y) + (a23.x + a23.y);
+      if (ENT) trun += (b01.x + b01.y) + (b23.x + b23.y);
+    }
+  }
+
+  __device__ __forceinline__ void end_unit(const Params& P, int, int split) {
+    if (grow < rows) {
+      const size_t o = (size_t)split * rows + grow;
+      P.part_m[o] = mrun * P.zl2;
+      P.part_s[o] = srun;
+      P.part_g[o] = grun;
+      if (ENT) P.part_t[o] = trun;
+    }
+  }
+};
+
+// Joins the column ranges' partials of 32 rows per block, 8 threads a row.
+// With M the largest scaled maximum and s the joined sum,
+//   logp = ln 2 (z_y zl2 - M - log2 s),  lse = ln 2 (M + log2 s),
+//   ent = ln 2 (log2 s - t / s):
+// the label's logit meets M before the logarithm is added, so that a
+// confident token's small log-probability is not the rest of two large terms.
+constexpr int kLogpMergeRows = 32, kLogpMergeLanes = 8;
+
+template <bool ENT>
+__global__ void __launch_bounds__(kLogpMergeRows * kLogpMergeLanes)
+logp_merge_kernel(const float* __restrict__ part_m, const float* __restrict__ part_s, const float* __restrict__ part_t,
+                  const float* __restrict__ part_g, const LiveRows* __restrict__ live,
+                  const int32_t* __restrict__ rowmap, float zl2, float* __restrict__ logp, float* __restrict__ lse,
+                  float* __restrict__ ent, const Status* __restrict__ status) {
+  __shared__ float s_m[kLogpMergeLanes][kLogpMergeRows], s_s[kLogpMergeLanes][kLogpMergeRows],
+      s_t[kLogpMergeLanes][kLogpMergeRows], s_g[kLogpMergeLanes][kLogpMergeRows];
+  const int rows = live->count, splits = live->raster.splits;
+  const int x = threadIdx.x & (kLogpMergeRows - 1), y = threadIdx.x / kLogpMergeRows;
+  const int q = blockIdx.x * kLogpMergeRows + x;
+  float m = -INFINITY, s = 0.f, t = 0.f, g = 0.f;
+  auto join = [&](float m2, float s2, float t2, float g2) {
+    const float top = fmaxf(m, m2);
+    const float d1 = m == top ? 0.f : m - top, d2 = m2 == top ? 0.f : m2 - top;
+    const float f1 = ex2_approx(d1), f2 = ex2_approx(d2);
+    if (ENT) t = (f1 > 0.f ? f1 * fmaf(d1, s, t) : 0.f) + (f2 > 0.f ? f2 * fmaf(d2, s2, t2) : 0.f);
+    s = fmaf(f1, s, f2 * s2);
+    g += g2;                                // the label's range holds it, the others 0
+    m = top;
+  };
+  if (q < rows)
+    for (int k = y; k < splits; k += kLogpMergeLanes) {
+      const size_t o = (size_t)k * rows + q;
+      join(part_m[o], part_s[o], ENT ? part_t[o] : 0.f, part_g[o]);
+    }
+  s_m[y][x] = m;
+  s_s[y][x] = s;
+  s_t[y][x] = t;
+  s_g[y][x] = g;
+  __syncthreads();
+  if (y == 0 && q < rows) {
+    for (int k = 1; k < kLogpMergeLanes && k < splits; ++k) join(s_m[k][x], s_s[k][x], s_t[k][x], s_g[k][x]);
+    const int n = rowmap[q];
+    const float l2 = log2f(s);
+    const bool failed = *reinterpret_cast<const volatile unsigned int*>(&status->timeout) != 0u;
+    const float nan = __int_as_float(0x7fc00000);
+    logp[n] = failed ? nan : kLn2 * (fmaf(g, zl2, -m) - l2);
+    lse[n] = failed ? nan : kLn2 * (m + l2);
+    if (ENT) ent[n] = failed ? nan : kLn2 * (l2 - t / s);
+  }
+}
+
+// Backward, per chunk: dZ in bf16 for the chunk's live rows (row-major, ldz
+// columns), stored as EpiDz stores it.  With u = z zl2 - lse log2(e), p = 2^u
+// and the factor 1 / T in g and h:
+//   without ENT  dZ = c (p - 1[v = y]), c = -g: |c| is folded into the
+//                exponent and the sign applied to the packed pairs;
+//   with ENT     dZ = p (a + b u) + g 1[v = y], a = -(g + h ent), b = -h ln 2.
+// The label's term is added before the rounding to bf16: p - 1 of a confident
+// token is small, and a rounded p would leave little of it.
+template <bool ENT>
+struct EpiDlogp {
+  static constexpr bool kStaging = true;
+  struct Params {
+    int row0;              // live-list index of chunk row 0
+    int V;
+    float zl2, zs;         // log2(e) / T and 1 / T
+    const int32_t *rowmap, *lab;
+    const float *lse, *ent, *dlogp, *dent;
+  };
+  float bias, a, b, add;
+  uint32_t sgn;
+  int label;
+
+  __device__ __forceinline__ void begin_unit(const Params& P, int r, int, int, const EpiCtx& cx) {
+    bias = 1e30f;            // rows past the live ones: p = 0 and a finite u
+    a = b = add = 0.f;
+    sgn = 0u;
+    label = -1;
+    if (r < cx.rows_valid) {
+      const int n = P.rowmap[P.row0 + r];
+      label = P.lab[P.row0 + r];
+      const float g = P.dlogp[n] * P.zs;
+      bias = P.lse[n] * kLog2e;
+      if (ENT) {
+        const float h = P.dent[n] * P.zs;
+        a = -fmaf(h, P.ent[n], g);
+        b = -h * kLn2;
+        add = g;
+      } else {
+        const float c = fabsf(g);
+        sgn = g > 0.f ? 0x80008000u : 0u;
+        bias -= log2f(c);
+        add = -c;
+      }
+    }
+  }
+  __device__ __forceinline__ void end_unit(const Params&, int, int) {}
+
+  __device__ __forceinline__ void tile(const Params& P, const CUtensorMap* out, int, int n, uint32_t taddr,
+                                       EpiCtx& cx) {
+    const float zl2 = P.zl2;
+#pragma unroll 1
+    for (int j = 0; j < BN / 64; ++j) {
+      float v[64];
+      __syncwarp();
+      tmem_ld_32x32b_x64(taddr + j * 64, v);
+      const int c0 = n * BN + j * 64;
+      const float2 zl2v = make_float2(zl2, zl2), nb = make_float2(-bias, -bias);
+      const float2 av = make_float2(a, a), bv = make_float2(b, b);
+#pragma unroll
+      for (int i = 0; i < 64; i += 2) {
+        const float2 u = __ffma2_rn(make_float2(v[i], v[i + 1]), zl2v, nb);
+        float2 e = make_float2(ex2_approx(u.x), ex2_approx(u.y));
+        if (ENT) e = __fmul2_rn(e, __ffma2_rn(bv, u, av));
+        v[i] = e.x;
+        v[i + 1] = e.y;
+      }
+      if (c0 + 64 > P.V) {                    // last vocabulary tile: zero columns >= V
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (c0 + i >= P.V) v[i] = 0.f;
+      }
+      const int off = label - c0;
+      if (__any_sync(0xffffffffu, (unsigned)off < 64u)) {     // a label in this group (rare)
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (i == off) v[i] += add;
+      }
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      if (!ENT && sgn) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] ^= sgn;
+      }
+      stage_store(cx, out, c0, cx.row_base, w, false);
+    }
+  }
+};
+
+// dW = dZ^T H of a single chunk, rounded to bf16 and stored (`out`: dW [V][d]
+// bf16, box {64, 128}, 128-byte swizzle): half the bytes of an fp32 dW, and
+// no pass that converts it.  Rounded once, from the fp32 accumulator.
+struct EpiDwHalf {
+  static constexpr bool kStaging = true;
+  struct Params {
+    int unused;
+  };
+  __device__ __forceinline__ void begin_unit(const Params&, int, int, int, const EpiCtx&) {}
+  __device__ __forceinline__ void end_unit(const Params&, int, int) {}
+
+  __device__ __forceinline__ void tile(const Params&, const CUtensorMap* out, int, int n, uint32_t taddr, EpiCtx& cx) {
+    const bool empty = cx.rows_valid == 0;    // no live rows: no MMA ran, the tile is zero
+#pragma unroll 1
+    for (int j = 0; j < BN / 64; ++j) {
+      float v[64];
+      __syncwarp();
+      if (empty) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) v[i] = 0.f;
+      } else {
+        tmem_ld_32x32b_x64(taddr + j * 64, v);
+      }
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      stage_store(cx, out, n * BN + j * 64, cx.row_base, w, false, kL2EvictFirst);
+    }
+  }
+};
+
+// out = bf16(in): the fp32 dW that several chunks added up.
+__global__ void __launch_bounds__(256) round_bf16_kernel(const float4* __restrict__ in, uint2* __restrict__ out, int64_t n4) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
+    const float4 f = in[i];
+    out[i] = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+  }
+}
+
+}  // namespace kd

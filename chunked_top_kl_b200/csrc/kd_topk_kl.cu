@@ -7,6 +7,10 @@
 //                      for each chunk of tokens: [gather_rows ->]
 //                      gemm<EpiDz> -> gemm<EpiDh + EpiDw> [-> scatter_rows]
 //                      (bracketed steps: skipping masked rows)
+// Label log-probabilities: label_prep -> gather_live -> gemm<EpiLogp> ->
+//                      logp_merge; gradient: label_prep -> for each chunk,
+//                      gather_live -> gemm<EpiDlogp> -> gemm<EpiDh + EpiDw or
+//                      EpiDwHalf> -> scatter_rows
 // Teacher top-K cache writer: for each chunk, gemm<EpiZ32> (fp32 logits and
 //                      their tile maxima) -> topk_select
 // The fused chunked loss of "Efficient Knowledge Distillation for LLMs"
@@ -22,10 +26,12 @@
 #include <atomic>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 
 #include "../../include/kd_topk_kl.h"
 #include "kd_gemm.cuh"
 #include "kd_small_kernels.cuh"
+#include "kd_token_logp.cuh"
 #include "kd_topk_select.cuh"
 
 using namespace kd;
@@ -162,7 +168,7 @@ struct DevInfo {
   int sms = 0;
   int pair_groups = 0;          // co-resident CTA pairs of the GEMM kernel
   int64_t l2_bytes = 0;
-  bool attr_set[8] = {};
+  bool attr_set[16] = {};     // by launch_gemm's slot
 };
 DevInfo g_dev[kMaxDevices];
 
@@ -825,6 +831,320 @@ int kd_teacher_topk(const void* Ht, const void* Wt, int64_t N, int64_t d, int64_
     if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
   }
   return KD_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- label log-probabilities
+//
+// What post-training losses need of the head: each token's log-probability of
+// its label (and the entropy of its distribution), and the gradients of H and
+// W for upstream gradients of both.  The same GEMMs as the distillation loss,
+// over the tokens that take part (see kd_token_logp.cuh).
+
+namespace {
+
+using ProbDwHalf = Prob<EpiDwHalf, true, true, kL2Normal, kL2EvictLast>;   // ProbDw with a bf16 result
+template <bool ENT>
+using ProbLogp = Prob<EpiLogp<ENT>, false, false, kL2EvictLast, kL2Normal>;
+template <bool ENT>
+using ProbDlogp = Prob<EpiDlogp<ENT>, false, false, kL2EvictLast, kL2Normal>;
+
+struct LogpLayout {
+  size_t off_status = 0, off_live = 0, off_rowmap = 0, off_lab = 0;
+  size_t off_part = 0, off_wave = 0, off_hc = 0;                       // forward
+  size_t off_jwave = 0, off_dz = 0, off_dhc = 0, off_dw32 = 0;         // backward
+  int64_t slots = 0, C = 0, ldz = 0, jwave_per_chunk = 0;
+  size_t total = 0;
+};
+
+// Status words first (as in the loss workspace, so kd_topk_kl_check reads them).
+LogpLayout make_logp_layout(int64_t N, int64_t d, int64_t V, int64_t chunk, bool backward, bool half_dW) {
+  LogpLayout L;
+  const int64_t n = N > 0 ? N : 1;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { size_t r = o; o = align256(o + bytes); return r; };
+  L.off_status = take(sizeof(Status));
+  L.off_live = take(sizeof(LiveRows));
+  L.off_rowmap = take(sizeof(int32_t) * (size_t)n);
+  L.off_lab = take(sizeof(int32_t) * (size_t)n);
+  if (!backward) {
+    L.slots = logp_part_slots(n);
+    L.off_part = take(4 * sizeof(float) * (size_t)L.slots);
+    L.off_wave = take(sizeof(unsigned int) * (size_t)wave_slots_bound(logp_units_bound(n), 0));
+    L.off_hc = take(2 * (size_t)n * d);
+  } else {
+    L.C = chunk < n ? chunk : n;
+    L.ldz = round_up(V, 8);
+    L.jwave_per_chunk =
+        wave_slots_bound(ceil_div(L.C, 256) * ceil_div(d, 256), ceil_div(V, 256) * ceil_div(d, 256));
+    L.off_jwave = take(sizeof(unsigned int) * (size_t)L.jwave_per_chunk * ceil_div(n, L.C));
+    L.off_dz = take(2 * (size_t)L.C * L.ldz);
+    L.off_hc = take(2 * (size_t)L.C * d);
+    L.off_dhc = take(2 * (size_t)L.C * d);
+    if (half_dW && n > L.C) L.off_dw32 = take(sizeof(float) * (size_t)V * d);
+  }
+  L.total = o;
+  return L;
+}
+
+// T is bounded so that a padding column's -1e30 stays finite in log2 units.
+int logp_checks(int64_t N, int64_t d, int64_t V, float T, int64_t chunk) {
+  if (N < 0 || d <= 0 || V <= 0 || chunk <= 0 || !(T > 0.f)) return KD_ERR_INVALID_ARG;
+  if (d % 8 != 0 || T < 1e-6f || T > 1e6f) return KD_ERR_UNSUPPORTED;
+  if (N >= (int64_t(1) << 31) || V >= (int64_t(1) << 31) || d >= (int64_t(1) << 24)) return KD_ERR_UNSUPPORTED;
+  return KD_OK;
+}
+
+int logp_common(const void* H, const void* W, const void* labels, int labels_i64, int64_t N, int64_t d, int64_t V,
+                float T, int64_t chunk, const void* ws) {
+  int st = logp_checks(N, d, V, T, chunk);
+  if (st != KD_OK) return st;
+  if (!W || !ws || (labels_i64 & ~1) || (N > 0 && (!H || !labels))) return KD_ERR_INVALID_ARG;
+  if (!aligned(W, 16) || !aligned(H, 16) || !aligned(ws, 256) || !aligned(labels, labels_i64 ? 8 : 4))
+    return KD_ERR_INVALID_ARG;
+  return KD_OK;
+}
+
+template <bool ENT>
+int logp_forward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, float T, float* logp, float* lse,
+                 float* ent, const LogpLayout& L, void* ws, int dev, cudaStream_t s, LabelPrep lp) {
+  const int groups = resident_groups(dev);
+  const int64_t n_tiles = ceil_div(V, BN), most = ceil_div(N, GeoP::TILE_M) * n_tiles;
+  LiveRows* live = at<LiveRows>(ws, L.off_live);
+  unsigned int* wave = at<unsigned int>(ws, L.off_wave);
+  lp.logp = logp;
+  lp.lse = lse;
+  lp.ent = ent;
+  lp.n_tiles = (int)n_tiles;
+  lp.groups = (int)(most < groups ? most : groups);
+  lp.max_splits = kLogpMaxSplits;
+  lp.part_slots = L.slots;
+  lp.band_bytes = GeoP::TILE_M * d * 2;
+  lp.l2_bytes = device_l2_bytes(dev);
+  lp.wave = wave;
+  label_prep_kernel<<<1, kLabelThreads, 0, s>>>(lp);
+  if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
+  void* hc = at<char>(ws, L.off_hc);
+  const unsigned copy_blocks = (unsigned)(device_sms(dev) * 8);
+  const int64_t want = ceil_div(N, 8);
+  gather_live_kernel<<<(unsigned)(want < copy_blocks ? want : copy_blocks), 256, 0, s>>>(
+      static_cast<const uint4*>(H), (int)(d / 8), lp.rowmap, live, 0, (int)N, static_cast<uint4*>(hc));
+  if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
+
+  CUtensorMap tmH, tmW;
+  if (!make_map(&tmH, hc, d, N, d, BK, BM) || !make_map(&tmW, W, d, V, d, BK, GeoP::B_ROWS)) return KD_ERR_CUDA;
+  ProbArgs a{};
+  a.raster.n_tiles = (int)n_tiles;
+  a.num_kb = (int)ceil_div(d, BK);
+  a.dyn_role = 4;
+  typename EpiLogp<ENT>::Params ep{};
+  ep.V = (int)V;
+  ep.zl2 = kLog2e / T;
+  ep.lab = lp.lab;
+  float* part = at<float>(ws, L.off_part);
+  ep.part_m = part;
+  ep.part_s = part + L.slots;
+  ep.part_g = part + 2 * L.slots;
+  ep.part_t = part + 3 * L.slots;
+  if (launch_one<ProbLogp<ENT>>(ENT ? 5 : 4, dev, lp.groups, tmH, tmW, tmH, a, lp.status, ep, s,
+                                DynRows{&live->count, 0, (int)N, &live->raster}, wave) != cudaSuccess)
+    return KD_ERR_CUDA;
+  logp_merge_kernel<ENT><<<(unsigned)ceil_div(N, kLogpMergeRows), kLogpMergeRows * kLogpMergeLanes, 0, s>>>(
+      ep.part_m, ep.part_s, ep.part_t, ep.part_g, live, lp.rowmap, ep.zl2, logp, lse, ent, lp.status);
+  return cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;
+}
+
+template <bool ENT>
+int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, float T, const float* lse,
+                  const float* ent, const float* dlogp, const float* dent, void* dH, void* dW, bool half_dW,
+                  bool accumulate_dW, const LogpLayout& L, void* ws, int dev, cudaStream_t s, LabelPrep lp) {
+  const int groups = resident_groups(dev);
+  const int64_t n_tiles = ceil_div(V, BN), C = L.C;
+  const int64_t most = ceil_div(C, GeoP::TILE_M) * n_tiles;
+  const int dz_groups = (int)(most < groups ? most : groups);
+  LiveRows* live = at<LiveRows>(ws, L.off_live);
+  lp.dlogp = dlogp;
+  lp.dent = dent;
+  lp.chunk = C;
+  lp.n_tiles = (int)n_tiles;
+  lp.groups = dz_groups;
+  lp.max_splits = kMaxDzSplits;
+  if (cudaMemsetAsync(dH, 0, sizeof(__nv_bfloat16) * (size_t)N * d, s) != cudaSuccess) return KD_ERR_CUDA;
+  label_prep_kernel<<<1, kLabelThreads, 0, s>>>(lp);
+  if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
+
+  const bool with_dW = dW != nullptr, rounds = half_dW && N > C;        // several chunks add up in fp32 first
+  void* dWacc = rounds ? static_cast<void*>(at<float>(ws, L.off_dw32)) : dW;
+  const bool half_store = half_dW && !rounds;
+  __nv_bfloat16* dz = at<__nv_bfloat16>(ws, L.off_dz);
+  void* hc = at<char>(ws, L.off_hc);
+  void* dhc = at<char>(ws, L.off_dhc);
+  unsigned int* jwave = at<unsigned int>(ws, L.off_jwave);
+  if (with_dW && cudaMemsetAsync(jwave, 0, sizeof(unsigned int) * (size_t)L.jwave_per_chunk * ceil_div(N, C), s) !=
+                     cudaSuccess)
+    return KD_ERR_CUDA;
+  CUtensorMap tmHk, tmWk, tmWmn, tmHmn, tmDH, tmDW;
+  if (!make_map(&tmHk, hc, d, C, d, BK, BM) || !make_map(&tmWk, W, d, V, d, BK, GeoP::B_ROWS) ||
+      !make_map(&tmWmn, W, d, V, d, 64, BK) || !make_map(&tmHmn, hc, d, C, d, 64, BK) ||
+      !make_map(&tmDH, dhc, d, C, d, 64, BM))
+    return KD_ERR_CUDA;
+  if (with_dW && !(half_store ? make_map(&tmDW, dWacc, d, V, d, 64, BM) : make_map(&tmDW, dWacc, d, V, d, 32, BM, true)))
+    return KD_ERR_CUDA;
+  const unsigned copy_blocks = (unsigned)(device_sms(dev) * 8);
+
+  for (int64_t c0 = 0; c0 < N; c0 += C) {
+    const int64_t Cc = (N - c0 < C) ? (N - c0) : C;
+    CUtensorMap tmZk, tmZmn;
+    if (!make_map(&tmZk, dz, L.ldz, Cc, L.ldz, BK, BM) || !make_map(&tmZmn, dz, L.ldz, Cc, L.ldz, 64, BK))
+      return KD_ERR_CUDA;
+    const DynRows dyn{&live->count, (int)c0, (int)Cc, &live->raster};
+    const int64_t want = ceil_div(Cc, 8);
+    const unsigned blocks = (unsigned)(want < copy_blocks ? want : copy_blocks);
+    gather_live_kernel<<<blocks, 256, 0, s>>>(static_cast<const uint4*>(H), (int)(d / 8), lp.rowmap, live, (int)c0,
+                                              (int)Cc, static_cast<uint4*>(hc));
+    if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
+
+    ProbArgs az{};
+    az.raster = forward_raster(ceil_div(Cc, GeoP::TILE_M), n_tiles, dz_groups, 0, 0, kMaxDzSplits);
+    az.num_kb = (int)ceil_div(d, BK);
+    az.dyn_role = 3;
+    typename EpiDlogp<ENT>::Params ez{};
+    ez.row0 = (int)c0;
+    ez.V = (int)V;
+    ez.zl2 = kLog2e / T;
+    ez.zs = 1.0f / T;
+    ez.rowmap = lp.rowmap;
+    ez.lab = lp.lab;
+    ez.lse = lse;
+    ez.ent = ent;
+    ez.dlogp = dlogp;
+    ez.dent = dent;
+    if (launch_one<ProbDlogp<ENT>>(ENT ? 7 : 6, dev, dz_groups, tmHk, tmWk, tmZk, az, lp.status, ez, s, dyn) !=
+        cudaSuccess)
+      return KD_ERR_CUDA;
+
+    // dH and dW of the chunk in one launch, as in the distillation loss's backward pass; dH alone without a dW
+    GemmArgs j{};
+    j.status = lp.status;
+    j.dyn = dyn;
+    const int64_t dh_cols = ceil_div(d, BN), dh_bands = ceil_div(Cc, GeoP::TILE_M);
+    const int64_t dw_units = with_dW ? ceil_div(V, GeoP::TILE_M) * dh_cols : 0;
+    const bool wide = wide_pays(dh_bands, dh_cols, ceil_div(V, BK), dw_units, ceil_div(Cc, BK), groups);
+    j.prob[0].raster = tile_raster(dh_bands, wide ? ceil_div(dh_cols, 2) : dh_cols, false);
+    j.prob[0].num_kb = (int)ceil_div(V, BK);
+    j.prob[0].dyn_role = 1;
+    j.prob[0].wide_cols = wide ? (int)dh_cols : 0;
+    EpiDh::Params eh{};
+    eh.row0 = 0;
+    cudaError_t e;
+    if (!with_dW) {
+      EpiNone::Params none{};
+      e = launch_gemm<ProbDh, NoProb, kPair>(9, dev, groups, tmZk, tmWmn, tmDH, tmZk, tmWmn, tmDH, j, eh, none, s);
+    } else {
+      j.prob[1].raster = tile_raster(ceil_div(V, GeoP::TILE_M), dh_cols, false);
+      j.prob[1].num_kb = (int)ceil_div(Cc, BK);
+      j.prob[1].dyn_role = 2;
+      plan_second_problem(j, groups);
+      if (j.prob[1].num_kb >= (wide ? kPaceKBlocksWide : kPaceKBlocks))
+        j.wave_sync = jwave + (size_t)(c0 / C) * L.jwave_per_chunk;
+      if (half_store) {
+        j.prob[1].dyn_zero_fill = 1;
+        EpiDwHalf::Params eb{};
+        e = launch_gemm<ProbDh, ProbDwHalf, kPair>(8, dev, groups, tmZk, tmWmn, tmDH, tmZmn, tmHmn, tmDW, j, eh, eb, s);
+      } else {
+        EpiDw::Params ew{};
+        ew.accumulate = ((accumulate_dW && !rounds) || c0 > 0) ? 1 : 0;
+        j.prob[1].dyn_zero_fill = ew.accumulate ? 0 : 1;
+        e = launch_gemm<ProbDh, ProbDw, kPair>(2, dev, groups, tmZk, tmWmn, tmDH, tmZmn, tmHmn, tmDW, j, eh, ew, s);
+      }
+    }
+    if (e != cudaSuccess) return KD_ERR_CUDA;
+    scatter_rows_kernel<<<blocks, 256, 0, s>>>(static_cast<const uint4*>(dhc), (int)(d / 8), lp.rowmap, &live->count,
+                                               (int)c0, (int)Cc, static_cast<uint4*>(dH));
+    if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
+  }
+  if (rounds) {
+    round_bf16_kernel<<<copy_blocks, 256, 0, s>>>(static_cast<const float4*>(dWacc), static_cast<uint2*>(dW), V * d / 4);
+    if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
+  }
+  return KD_OK;
+}
+
+LabelPrep label_prep(const void* labels, int labels_i64, int64_t N, int64_t V, const LogpLayout& L, void* ws) {
+  LabelPrep lp{};
+  lp.labels = labels;
+  lp.labels_i64 = labels_i64;
+  lp.N = (int)N;
+  lp.V = (int)V;
+  lp.rowmap = at<int32_t>(ws, L.off_rowmap);
+  lp.lab = at<int32_t>(ws, L.off_lab);
+  lp.live = at<LiveRows>(ws, L.off_live);
+  lp.status = at<Status>(ws, L.off_status);
+  return lp;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kd_token_logp_forward_workspace_size(int64_t N, int64_t d, int64_t V) {
+  if (logp_checks(N, d, V, 1.0f, 1) != KD_OK) return 0;
+  return make_logp_layout(N, d, V, 1, false, false).total;
+}
+
+size_t kd_token_logp_backward_workspace_size(int64_t N, int64_t d, int64_t V, int64_t chunk, int dW_bf16) {
+  if (logp_checks(N, d, V, 1.0f, chunk) != KD_OK || (dW_bf16 & ~1)) return 0;
+  return make_logp_layout(N, d, V, chunk, true, dW_bf16 != 0).total;
+}
+
+int kd_token_logp_forward(const void* H, const void* W, const void* labels, int labels_i64, int64_t N, int64_t d,
+                          int64_t V, float T, float* logp, float* lse, float* entropy, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  int st = logp_common(H, W, labels, labels_i64, N, d, V, T, 1, workspace);
+  if (st != KD_OK) return st;
+  if (N > 0 && (!logp || !lse)) return KD_ERR_INVALID_ARG;
+  if (!aligned(logp, 4) || !aligned(lse, 4) || !aligned(entropy, 4)) return KD_ERR_INVALID_ARG;
+  const LogpLayout L = make_logp_layout(N, d, V, 1, false, false);
+  if (workspace_bytes < L.total) return KD_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (N == 0)
+    return cudaMemsetAsync(at<Status>(workspace, L.off_status), 0, sizeof(Status), s) == cudaSuccess ? KD_OK
+                                                                                                     : KD_ERR_CUDA;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KD_ERR_CUDA;
+  const LabelPrep lp = label_prep(labels, labels_i64, N, V, L, workspace);
+  return entropy ? logp_forward<true>(H, W, N, d, V, T, logp, lse, entropy, L, workspace, dev, s, lp)
+                 : logp_forward<false>(H, W, N, d, V, T, logp, lse, nullptr, L, workspace, dev, s, lp);
+}
+
+int kd_token_logp_backward(const void* H, const void* W, const void* labels, int labels_i64, int64_t N, int64_t d,
+                           int64_t V, float T, int64_t chunk, const float* lse, const float* entropy,
+                           const float* dlogp, const float* dentropy, void* dH, void* dW, int dW_bf16,
+                           int accumulate_dW, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = logp_common(H, W, labels, labels_i64, N, d, V, T, chunk, workspace);
+  if (st != KD_OK) return st;
+  if ((dW_bf16 & ~1) || (dW_bf16 && accumulate_dW)) return KD_ERR_INVALID_ARG;
+  if (N > 0 && (!lse || !dlogp || !dH || (dentropy && !entropy))) return KD_ERR_INVALID_ARG;
+  if (!aligned(dH, 16) || !aligned(dW, 16)) return KD_ERR_INVALID_ARG;
+  for (const float* p : {lse, entropy, dlogp, dentropy})
+    if (!aligned(p, 4)) return KD_ERR_INVALID_ARG;
+  const LogpLayout L = make_logp_layout(N, d, V, chunk, true, dW_bf16 != 0);
+  if (workspace_bytes < L.total) return KD_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (N == 0) {
+    if (cudaMemsetAsync(at<Status>(workspace, L.off_status), 0, sizeof(Status), s) != cudaSuccess) return KD_ERR_CUDA;
+    if (dW && !accumulate_dW && cudaMemsetAsync(dW, 0, (dW_bf16 ? 2 : 4) * (size_t)V * d, s) != cudaSuccess)
+      return KD_ERR_CUDA;
+    return KD_OK;
+  }
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KD_ERR_CUDA;
+  const LabelPrep lp = label_prep(labels, labels_i64, N, V, L, workspace);
+  return dentropy ? logp_backward<true>(H, W, N, d, V, T, lse, entropy, dlogp, dentropy, dH, dW, dW_bf16 != 0,
+                                        accumulate_dW != 0, L, workspace, dev, s, lp)
+                  : logp_backward<false>(H, W, N, d, V, T, lse, entropy, dlogp, nullptr, dH, dW, dW_bf16 != 0,
+                                         accumulate_dW != 0, L, workspace, dev, s, lp);
 }
 
 }  // extern "C"

@@ -275,6 +275,43 @@ int kd_teacher_topk(const void* Ht, const void* Wt, int64_t N, int64_t d, int64_
                     int64_t chunk, int32_t* topk_idx, float* topk_logit,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* Label log-probabilities under the head, for losses on labels, preferences
+ * and rewards.  For labels y (int32 [N], or int64 when labels_i64 is 1) and
+ * temperature T (1e-6 <= T <= 1e6) writes, per token,
+ *   z = H W^T / T,  lse[n] = log sum_v exp(z[n,v])
+ *   logp[n] = z[n, y[n]] - lse[n]
+ *   entropy[n] = lse[n] - sum_v softmax(z[n])[v] z[n,v]    (entropy may be NULL)
+ * A negative label marks a token without one (a prompt token): its logp, lse
+ * and entropy are 0 and its row is not computed.  A label >= V gives NaN, is
+ * counted in the workspace and reported by kd_topk_kl_check as
+ * KD_ERR_BAD_INDEX.  The tokens with a label are gathered on the device (N x d
+ * bf16 of workspace); no logits are stored.  When a pipeline wait times out
+ * the outputs are NaN. */
+size_t kd_token_logp_forward_workspace_size(int64_t N, int64_t d, int64_t V);
+int kd_token_logp_forward(const void* H, const void* W, const void* labels, int labels_i64,
+                          int64_t N, int64_t d, int64_t V, float T,
+                          float* logp, float* lse, float* entropy,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of the above for upstream gradients dlogp[N] and dentropy[N]
+ * (NULL for none; otherwise entropy must be the forward pass's output):
+ *   dZ[n,v] = (1 / T) (dlogp[n] (1[v = y[n]] - p[n,v])
+ *                      - dentropy[n] p[n,v] (log p[n,v] + entropy[n]))
+ *   dH = dZ W (bf16 [N][d], overwritten),  dW = dZ^T H
+ * with p recomputed from lse, `chunk` tokens at a time; dZ is rounded to bf16
+ * before the two products.  Tokens without a valid label and tokens whose
+ * upstream gradients are 0 are left out (their dH rows are 0).  dW is fp32
+ * [V][d] (overwritten, or added to with accumulate_dW = 1), or bf16 [V][d]
+ * with dW_bf16 = 1 (overwritten; rounded once, after the sum over all
+ * chunks), or NULL: dH alone. */
+size_t kd_token_logp_backward_workspace_size(int64_t N, int64_t d, int64_t V, int64_t chunk, int dW_bf16);
+int kd_token_logp_backward(const void* H, const void* W, const void* labels, int labels_i64,
+                           int64_t N, int64_t d, int64_t V, float T, int64_t chunk,
+                           const float* lse, const float* entropy,
+                           const float* dlogp, const float* dentropy,
+                           void* dH, void* dW, int dW_bf16, int accumulate_dW,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------------------
  * Losses over token log-probabilities.  The arrays are fp32 [N], the tokens
  * of S sequences: sequence s is [offsets[s], offsets[s + 1]) with offsets
