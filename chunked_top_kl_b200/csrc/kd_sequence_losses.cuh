@@ -25,7 +25,9 @@ namespace seq {
 
 constexpr int kThreads = 256;
 constexpr int kSumBlocks = 592;      // blocks of the first launch at most (4 per SM): partial totals to join
-constexpr int kLossBlocks = 1184;    // blocks of the second launch at most (8 per SM)
+constexpr int kLossBlocks = 4736;    // blocks of the second launch at most (32 per SM, several of them in turn)
+constexpr int kSumUnroll = 4;        // groups of four tokens whose loads a thread has in flight, first launch
+constexpr int kLossUnroll = 2;       // and second
 
 // The sequences of an array of N tokens: sequence s is [offsets[s],
 // offsets[s + 1]), or row s of S rows of L tokens when offsets is null.
@@ -188,17 +190,23 @@ __global__ void __launch_bounds__(kThreads) pref_sums_kernel(const PrefArgs A) {
     int64_t lo, hi;
     item_range(A.q, s, (int)(it - s * A.q.splits), lo, hi);
     double r = 0.0, n = 0.0;
-    for (int64_t t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM) {
-      float m[4], lp[4], rf[4] = {0.f, 0.f, 0.f, 0.f};
-      load_mask4<VEC>(A.mask, t0, lo, hi, m);
-      load4<VEC>(A.logp, t0, lo, hi, lp);
-      if (A.ref) load4<VEC>(A.ref, t0, lo, hi, rf);
+    for (int64_t t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM * kSumUnroll) {
+      float m[kSumUnroll][4], lp[kSumUnroll][4], rf[kSumUnroll][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (m[j] != 0.f) {                    // a masked place may hold anything, NaN included
-          r += (double)m[j] * ((double)lp[j] - (double)rf[j]);
-          n += (double)m[j];
-        }
+      for (int u = 0; u < kSumUnroll; ++u) {
+        const int64_t t = t0 + 4 * TEAM * u;
+        load_mask4<VEC>(A.mask, t, lo, hi, m[u]);
+        load4<VEC>(A.logp, t, lo, hi, lp[u]);
+        if (A.ref) load4<VEC>(A.ref, t, lo, hi, rf[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kSumUnroll; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (m[u][j] != 0.f) {               // a masked place may hold anything, NaN included
+            r += (double)m[u][j] * ((double)lp[u][j] - (A.ref ? (double)rf[u][j] : 0.0));
+            n += (double)m[u][j];
+          }
     }
     r = team_sum<TEAM>(r, red);
     n = team_sum<TEAM>(n, red);
@@ -274,12 +282,18 @@ __global__ void __launch_bounds__(kThreads) pref_loss_kernel(const PrefArgs A) {
     }
     int64_t lo, hi;
     item_range(A.q, s, k, lo, hi);
-    for (int64_t t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM) {
-      float m[4], d[4];
-      load_mask4<VEC>(A.mask, t0, lo, hi, m);
+    for (int64_t t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM * kSumUnroll) {
+      float m[kSumUnroll][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) d[j] = m[j] != 0.f ? coef * m[j] : 0.f;
-      store4<VEC>(A.dlogp, t0, lo, hi, d);
+      for (int u = 0; u < kSumUnroll; ++u) load_mask4<VEC>(A.mask, t0 + 4 * TEAM * u, lo, hi, m[u]);
+#pragma unroll
+      for (int u = 0; u < kSumUnroll; ++u) {
+        const int64_t t = t0 + 4 * TEAM * u;
+        float d[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = m[u][j] != 0.f ? coef * m[u][j] : 0.f;
+        if (t < hi) store4<VEC>(A.dlogp, t, lo, hi, d);
+      }
     }
   }
   if (A.dlogp) zero_outside(A.q, A.dlogp);
@@ -342,10 +356,13 @@ __global__ void __launch_bounds__(kThreads) policy_sums_kernel(const PolicyArgs 
     item_range(A.q, s, (int)(it - s * A.q.splits), lo, hi);
     double n = 0.0;
     if (A.mask) {
-      for (int64_t t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM) {
-        float m[4];
-        load4<VEC>(A.mask, t0, lo, hi, m);
-        n += ((double)m[0] + (double)m[1]) + ((double)m[2] + (double)m[3]);
+      for (int64_t t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM * kSumUnroll) {
+        float m[kSumUnroll][4];
+#pragma unroll
+        for (int u = 0; u < kSumUnroll; ++u) load4<VEC>(A.mask, t0 + 4 * TEAM * u, lo, hi, m[u]);
+#pragma unroll
+        for (int u = 0; u < kSumUnroll; ++u)
+          n += ((double)m[u][0] + (double)m[u][1]) + ((double)m[u][2] + (double)m[u][3]);
       }
       n = team_sum<TEAM>(n, red);
     } else {
@@ -444,31 +461,41 @@ __global__ void __launch_bounds__(kThreads) policy_loss_kernel(const PolicyArgs 
     const float wg = (float)w * g;
     const float as = A.adv_per_seq ? A.adv[s] : 0.f;
     double il = 0.0, ik = 0.0, ic = 0.0;
-    for (int64_t t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM) {
-      float m[4], d[4] = {0.f, 0.f, 0.f, 0.f};
-      load_mask4<VEC>(A.mask, t0, lo, hi, m);
-      if (m[0] != 0.f || m[1] != 0.f || m[2] != 0.f || m[3] != 0.f) {
-        float lp[4], od[4], rf[4] = {0.f, 0.f, 0.f, 0.f}, a[4] = {as, as, as, as};
-        load4<VEC>(A.logp, t0, lo, hi, lp);
-        load4<VEC>(A.old, t0, lo, hi, od);
-        if (A.ref) load4<VEC>(A.ref, t0, lo, hi, rf);
-        if (!A.adv_per_seq) load4<VEC>(A.adv, t0, lo, hi, a);
-        float l4 = 0.f, k4 = 0.f, c4 = 0.f;
+    for (int64_t t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM * kLossUnroll) {
+      float m[kLossUnroll][4], lp[kLossUnroll][4], od[kLossUnroll][4], rf[kLossUnroll][4], a[kLossUnroll][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (m[j] != 0.f) {                  // a masked place may hold anything, NaN included
+      for (int u = 0; u < kLossUnroll; ++u) load_mask4<VEC>(A.mask, t0 + 4 * TEAM * u, lo, hi, m[u]);
+#pragma unroll
+      for (int u = 0; u < kLossUnroll; ++u) {
+        const int64_t t = t0 + 4 * TEAM * u;
+        if (m[u][0] != 0.f || m[u][1] != 0.f || m[u][2] != 0.f || m[u][3] != 0.f) {   // padding costs its mask alone
+          load4<VEC>(A.logp, t, lo, hi, lp[u]);
+          load4<VEC>(A.old, t, lo, hi, od[u]);
+          if (A.ref) load4<VEC>(A.ref, t, lo, hi, rf[u]);
+          if (!A.adv_per_seq) load4<VEC>(A.adv, t, lo, hi, a[u]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kLossUnroll; ++u) {
+        const int64_t t = t0 + 4 * TEAM * u;
+        float d[4], l4 = 0.f, k4 = 0.f, c4 = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          d[j] = 0.f;
+          if (m[u][j] != 0.f) {               // a masked place may hold anything, NaN included
             float l, k, c, dd;
-            policy_token(A, lp[j], od[j], rf[j], a[j], l, k, c, dd);
-            l4 = fmaf(m[j], l, l4);
-            k4 = fmaf(m[j], k, k4);
-            c4 = fmaf(m[j], c, c4);
-            d[j] = wg * m[j] * dd;
+            policy_token(A, lp[u][j], od[u][j], rf[u][j], A.adv_per_seq ? as : a[u][j], l, k, c, dd);
+            l4 = fmaf(m[u][j], l, l4);
+            k4 = fmaf(m[u][j], k, k4);
+            c4 = fmaf(m[u][j], c, c4);
+            d[j] = wg * m[u][j] * dd;
           }
+        }
         il += (double)l4;
         ik += (double)k4;
         ic += (double)c4;
+        if (A.dlogp && t < hi) store4<VEC>(A.dlogp, t, lo, hi, d);
       }
-      if (A.dlogp) store4<VEC>(A.dlogp, t0, lo, hi, d);
     }
     sum_l += w != 0.0 ? w * il : 0.0;
     sum_k += w != 0.0 ? w * ik : 0.0;

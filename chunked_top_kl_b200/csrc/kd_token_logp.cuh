@@ -24,6 +24,15 @@ namespace kd {
 constexpr int kLabelThreads = 1024;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// The tensor cores' fp32 accumulation truncates at every step, so a logit that
+// they return is short of the exact one by a share of itself that grows with
+// the number of steps.  Measured over random and drifting rows, the mean of
+// (z - z_exact) / z_exact is -d 2^-23 times 0.0064 (d = 256), 0.0075 (2048),
+// 0.0081 (8192), the same for small and large logits: 2.6e-6 at d = 2880, two
+// fp32 steps, and always the same way, so it would add up over a sequence's
+// tokens.  The logits' scale makes up for the mean.
+__host__ __device__ __forceinline__ double accumulation_gain(int64_t d) { return 1.0 + 0.0077 * (double)d / 8388608.0; }
+
 // What the label scan leaves for the kernels behind it.
 struct LiveRows {
   int count;         // rows that take part
@@ -136,26 +145,64 @@ __global__ void __launch_bounds__(kLabelThreads) label_prep_kernel(const LabelPr
     for (int64_t i = t; i < wave_slots_bound(r.num_units, 0); i += kLabelThreads) P.wave[i] = 0u;
 }
 
+__device__ __forceinline__ float dot8(const uint4& x, const uint4& y) {
+  const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+  float s[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {           // bf16 is the upper half of an fp32; products are exact
+    const float lo = __uint_as_float(a[k] << 16) * __uint_as_float(b[k] << 16);
+    s[k] = fmaf(__uint_as_float(a[k] & 0xffff0000u), __uint_as_float(b[k] & 0xffff0000u), lo);
+  }
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
 // Rows [row0, row0 + C) of the live list: dst[r] = src[rowmap[row0 + r]]
 // (16-byte vectors, d8 per row), a warp per row.  Rows past the live ones are
 // zero up to the end of the last band of 256, as far as the GEMMs read.
+//
+// With zlab (the forward pass) each row's label logit H[n] W[lab] is taken on
+// the way, in 64-bit partial sums: it enters the log-probability undiminished,
+// and the tensor cores return a logit of ten some 1e-5 off at d = 2880.  W's
+// rows are read beside H's, 2 d more bytes a row.
+//
+// Of the first rows, kPadRows are written even when fewer are live: loads of a
+// band with a row or two made the one-token product 1.4 times slower (294 us
+// against 207 us at d = 2880, 1.07 GB of W) than those of 64 rows.
+constexpr int kPadRows = 64;
+
 __global__ void __launch_bounds__(256)
 gather_live_kernel(const uint4* __restrict__ src, int d8, const int32_t* __restrict__ rowmap,
-                   const LiveRows* __restrict__ live, int row0, int C, uint4* __restrict__ dst) {
+                   const LiveRows* __restrict__ live, int row0, int C, uint4* __restrict__ dst,
+                   const uint4* __restrict__ W, const int32_t* __restrict__ lab, float* __restrict__ zlab) {
   int rows = live->count - row0;
   rows = rows < 0 ? 0 : (rows > C ? C : rows);
-  const int64_t end = ceil_div64(rows, 256) * 256 < C ? ceil_div64(rows, 256) * 256 : C;
+  const int64_t room = C > kPadRows ? C : kPadRows, want = ceil_div64(rows, 256) * 256;
+  const int64_t end = want < room ? want : room;
+  const int lane = threadIdx.x & 31;
   for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < end; r += (int64_t)gridDim.x * 8) {
-    const uint4* from = r < rows ? src + (size_t)rowmap[row0 + r] * d8 : nullptr;
-    for (int j = threadIdx.x & 31; j < d8; j += 32)
-      dst[(size_t)r * d8 + j] = from ? from[j] : make_uint4(0u, 0u, 0u, 0u);
+    if (r >= rows) {
+      for (int j = lane; j < d8; j += 32) dst[(size_t)r * d8 + j] = make_uint4(0u, 0u, 0u, 0u);
+      continue;
+    }
+    const uint4* from = src + (size_t)rowmap[row0 + r] * d8;
+    const uint4* w = zlab ? W + (size_t)lab[row0 + r] * d8 : nullptr;
+    double z = 0.0;
+    for (int j = lane; j < d8; j += 32) {
+      const uint4 h = from[j];
+      dst[(size_t)r * d8 + j] = h;
+      if (w) z += (double)dot8(h, w[j]);
+    }
+    if (w) {
+      z = warp_sum_d(z);
+      if (lane == 0) zlab[row0 + r] = (float)z;
+    }
   }
 }
 
 // Forward: running scaled maximum and sum-exp over the unit's vocabulary
 // columns, the label's logit, and with ENT the sum of e u that the entropy
-// needs.  In log2 units, u_v = z_v zl2 - mb with zl2 = log2(e) / T and
-// mb = max z * zl2 as rounded: s = sum 2^u and t = sum 2^u u (u <= 0, so t
+// needs.  In log2 units, u_v = z_v zl2 - mb with zl2 = log2(e) / T (times
+// accumulation_gain) and mb = max z * zl2 as rounded: s = sum 2^u and t = sum 2^u u (u <= 0, so t
 // does not cancel).  A new maximum shifts u by delta = mb_old - mb_new:
 // t <- 2^delta (t + delta s), s <- 2^delta s.  Partials (mb, s, t, label
 // logit) per live row and column range; columns >= V are taken as -1e30.
@@ -243,8 +290,12 @@ struct EpiLogp {
 };
 
 // Joins the column ranges' partials of 32 rows per block, 8 threads a row.
-// With M the largest scaled maximum and s the joined sum,
-//   logp = ln 2 (z_y zl2 - M - log2 s),  lse = ln 2 (M + log2 s),
+// The label's term is then exchanged for that of its exact logit z_y (see
+// gather_live_kernel; the products' own g serves to take the old term out):
+// with u = g zl2 - M, u' = z_y log2(e) / T - M,
+//   s <- s + 2^u (2^(u' - u) - 1),  t <- t + 2^u' u' - 2^u u.
+// With M the largest scaled maximum,
+//   logp = ln 2 (u' - log2 s),  lse = ln 2 (M + log2 s),
 //   ent = ln 2 (log2 s - t / s):
 // the label's logit meets M before the logarithm is added, so that a
 // confident token's small log-probability is not the rest of two large terms.
@@ -254,7 +305,8 @@ template <bool ENT>
 __global__ void __launch_bounds__(kLogpMergeRows * kLogpMergeLanes)
 logp_merge_kernel(const float* __restrict__ part_m, const float* __restrict__ part_s, const float* __restrict__ part_t,
                   const float* __restrict__ part_g, const LiveRows* __restrict__ live,
-                  const int32_t* __restrict__ rowmap, float zl2, float* __restrict__ logp, float* __restrict__ lse,
+                  const int32_t* __restrict__ rowmap, const float* __restrict__ zlab, float zl2, float zl2_exact,
+                  float* __restrict__ logp, float* __restrict__ lse,
                   float* __restrict__ ent, const Status* __restrict__ status) {
   __shared__ float s_m[kLogpMergeLanes][kLogpMergeRows], s_s[kLogpMergeLanes][kLogpMergeRows],
       s_t[kLogpMergeLanes][kLogpMergeRows], s_g[kLogpMergeLanes][kLogpMergeRows];
@@ -284,10 +336,14 @@ logp_merge_kernel(const float* __restrict__ part_m, const float* __restrict__ pa
   if (y == 0 && q < rows) {
     for (int k = 1; k < kLogpMergeLanes && k < splits; ++k) join(s_m[k][x], s_s[k][x], s_t[k][x], s_g[k][x]);
     const int n = rowmap[q];
+    const float ug = fmaf(g, zl2, -m), uy = fmaf(zlab[q], zl2_exact, -m);
+    const float eg = exp2f(ug), more = eg * expm1f((uy - ug) * kLn2);
+    s += more;
+    if (ENT) t += fmaf(more, uy, eg * (uy - ug));
     const float l2 = log2f(s);
     const bool failed = *reinterpret_cast<const volatile unsigned int*>(&status->timeout) != 0u;
     const float nan = __int_as_float(0x7fc00000);
-    logp[n] = failed ? nan : kLn2 * (fmaf(g, zl2, -m) - l2);
+    logp[n] = failed ? nan : kLn2 * (uy - l2);
     lse[n] = failed ? nan : kLn2 * (m + l2);
     if (ENT) ent[n] = failed ? nan : kLn2 * (l2 - t / s);
   }
@@ -307,7 +363,7 @@ struct EpiDlogp {
   struct Params {
     int row0;              // live-list index of chunk row 0
     int V;
-    float zl2, zs;         // log2(e) / T and 1 / T
+    float zl2, zs;         // log2(e) / T (times accumulation_gain) and 1 / T
     const int32_t *rowmap, *lab;
     const float *lse, *ent, *dlogp, *dent;
   };

@@ -852,7 +852,7 @@ using ProbDlogp = Prob<EpiDlogp<ENT>, false, false, kL2EvictLast, kL2Normal>;
 
 struct LogpLayout {
   size_t off_status = 0, off_live = 0, off_rowmap = 0, off_lab = 0;
-  size_t off_part = 0, off_wave = 0, off_hc = 0;                       // forward
+  size_t off_part = 0, off_wave = 0, off_zlab = 0, off_hc = 0;         // forward
   size_t off_jwave = 0, off_dz = 0, off_dhc = 0, off_dw32 = 0;         // backward
   int64_t slots = 0, C = 0, ldz = 0, jwave_per_chunk = 0;
   size_t total = 0;
@@ -872,7 +872,8 @@ LogpLayout make_logp_layout(int64_t N, int64_t d, int64_t V, int64_t chunk, bool
     L.slots = logp_part_slots(n);
     L.off_part = take(4 * sizeof(float) * (size_t)L.slots);
     L.off_wave = take(sizeof(unsigned int) * (size_t)wave_slots_bound(logp_units_bound(n), 0));
-    L.off_hc = take(2 * (size_t)n * d);
+    L.off_zlab = take(sizeof(float) * (size_t)n);
+    L.off_hc = take(2 * (size_t)(n > kPadRows ? n : kPadRows) * d);
   } else {
     L.C = chunk < n ? chunk : n;
     L.ldz = round_up(V, 8);
@@ -880,7 +881,7 @@ LogpLayout make_logp_layout(int64_t N, int64_t d, int64_t V, int64_t chunk, bool
         wave_slots_bound(ceil_div(L.C, 256) * ceil_div(d, 256), ceil_div(V, 256) * ceil_div(d, 256));
     L.off_jwave = take(sizeof(unsigned int) * (size_t)L.jwave_per_chunk * ceil_div(n, L.C));
     L.off_dz = take(2 * (size_t)L.C * L.ldz);
-    L.off_hc = take(2 * (size_t)L.C * d);
+    L.off_hc = take(2 * (size_t)(L.C > kPadRows ? L.C : kPadRows) * d);
     L.off_dhc = take(2 * (size_t)L.C * d);
     if (half_dW && n > L.C) L.off_dw32 = take(sizeof(float) * (size_t)V * d);
   }
@@ -926,21 +927,23 @@ int logp_forward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, 
   label_prep_kernel<<<1, kLabelThreads, 0, s>>>(lp);
   if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
   void* hc = at<char>(ws, L.off_hc);
+  float* zlab = at<float>(ws, L.off_zlab);
   const unsigned copy_blocks = (unsigned)(device_sms(dev) * 8);
-  const int64_t want = ceil_div(N, 8);
+  const int64_t want = ceil_div(N > kPadRows ? N : kPadRows, 8);
   gather_live_kernel<<<(unsigned)(want < copy_blocks ? want : copy_blocks), 256, 0, s>>>(
-      static_cast<const uint4*>(H), (int)(d / 8), lp.rowmap, live, 0, (int)N, static_cast<uint4*>(hc));
+      static_cast<const uint4*>(H), (int)(d / 8), lp.rowmap, live, 0, (int)N, static_cast<uint4*>(hc),
+      static_cast<const uint4*>(W), lp.lab, zlab);
   if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
 
   CUtensorMap tmH, tmW;
-  if (!make_map(&tmH, hc, d, N, d, BK, BM) || !make_map(&tmW, W, d, V, d, BK, GeoP::B_ROWS)) return KD_ERR_CUDA;
+  if (!make_map(&tmH, hc, d, N > kPadRows ? N : kPadRows, d, BK, BM) || !make_map(&tmW, W, d, V, d, BK, GeoP::B_ROWS)) return KD_ERR_CUDA;
   ProbArgs a{};
   a.raster.n_tiles = (int)n_tiles;
   a.num_kb = (int)ceil_div(d, BK);
   a.dyn_role = 4;
   typename EpiLogp<ENT>::Params ep{};
   ep.V = (int)V;
-  ep.zl2 = kLog2e / T;
+  ep.zl2 = (float)(1.4426950408889634 / T * accumulation_gain(d));
   ep.lab = lp.lab;
   float* part = at<float>(ws, L.off_part);
   ep.part_m = part;
@@ -951,7 +954,7 @@ int logp_forward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, 
                                 DynRows{&live->count, 0, (int)N, &live->raster}, wave) != cudaSuccess)
     return KD_ERR_CUDA;
   logp_merge_kernel<ENT><<<(unsigned)ceil_div(N, kLogpMergeRows), kLogpMergeRows * kLogpMergeLanes, 0, s>>>(
-      ep.part_m, ep.part_s, ep.part_t, ep.part_g, live, lp.rowmap, ep.zl2, logp, lse, ent, lp.status);
+      ep.part_m, ep.part_s, ep.part_t, ep.part_g, live, lp.rowmap, zlab, ep.zl2, kLog2e / T, logp, lse, ent, lp.status);
   return cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;
 }
 
@@ -1002,7 +1005,7 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
     const int64_t want = ceil_div(Cc, 8);
     const unsigned blocks = (unsigned)(want < copy_blocks ? want : copy_blocks);
     gather_live_kernel<<<blocks, 256, 0, s>>>(static_cast<const uint4*>(H), (int)(d / 8), lp.rowmap, live, (int)c0,
-                                              (int)Cc, static_cast<uint4*>(hc));
+                                              (int)Cc, static_cast<uint4*>(hc), nullptr, nullptr, nullptr);
     if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
 
     ProbArgs az{};
@@ -1012,7 +1015,7 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
     typename EpiDlogp<ENT>::Params ez{};
     ez.row0 = (int)c0;
     ez.V = (int)V;
-    ez.zl2 = kLog2e / T;
+    ez.zl2 = (float)(1.4426950408889634 / T * accumulation_gain(d));
     ez.zs = 1.0f / T;
     ez.rowmap = lp.rowmap;
     ez.lab = lp.lab;

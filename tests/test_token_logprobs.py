@@ -79,9 +79,9 @@ def test_workspace_sizes(kd):
     for bad in ((-1, 64, 100), (1, 60, 100), (1, 0, 100), (1, 64, 0), (1 << 31, 64, 100), (1, 64, 1 << 31)):
         assert f(*bad) == 0 and b(*bad, 128, 0) == 0
     assert b(10, 64, 100, 0, 0) == 0 and b(10, 64, 100, 128, 2) == 0
-    # linear in N: the gathered rows, 4 partials of 16 ranges, the token list and labels, pacing counters
+    # linear in N: the gathered rows, 4 partials of 16 ranges, the token list, labels and their logits, pacing counters
     d = 2048
-    per = 2 * d + 4 * 4 * 16 + 8 + 4 * 2 // 8
+    per = 2 * d + 4 * 4 * 16 + 12 + 4 * 2 // 8
     assert abs((f(1 << 16, d, 128256) - f(1 << 15, d, 128256)) / (1 << 15) - per) < 0.1
     # one chunk writes a bf16 dW directly; several need an fp32 one
     assert b(4096, d, 128256, 4096, 1) == b(4096, d, 128256, 4096, 0)
