@@ -71,13 +71,16 @@ struct ProbArgs {
   int dyn_bands_fastest;
   int dyn_zero_fill;    // role 2 with no live rows: still write the (zero) output tiles
   int wide_cols;        // > 0: wide units (Prob WIDE): its 256-column tiles; the raster counts pairs of them
+  int k_splits;         // Prob KSPLIT: K ranges per tile (at least 1); raster column n is column
+  int k_cols;           // n % k_cols of K range n / k_cols
 };
 
 // K blocks of MMA work per unit of a problem, the joint schedule's cost: a
 // wide unit's K block runs two MMA blocks (one per column tile).  A problem
 // declared WIDE runs wide units when the launch sets wide_cols.
 KD_HD int64_t unit_cost(const ProbArgs& pa) {
-  return (int64_t)pa.raster.tiles_per_split * pa.num_kb * (pa.wide_cols > 0 ? 2 : 1);
+  const int64_t kb = pa.k_splits > 1 ? ceil_div64(pa.num_kb, pa.k_splits) : pa.num_kb;
+  return (int64_t)pa.raster.tiles_per_split * kb * (pa.wide_cols > 0 ? 2 : 1);
 }
 
 // A launch over rows whose number is known only on the device (a chunk of the
@@ -91,6 +94,7 @@ struct DynRows {
   const Raster* raster; // roles 3 and 4: the schedule of the live rows (role 4) or of a chunk that
                         // they fill in part (role 3), worked out by an earlier kernel; may be null
                         // for role 3
+  const DhPlan* plan;   // role 1 of a KSPLIT problem: how such a chunk's tiles are cut
 };
 
 // A launch runs problem 0 and, optionally, problem 1.  Problem 0's units go
@@ -129,6 +133,13 @@ __device__ __forceinline__ void apply_live_rows(GemmArgs& a, int rows, int ngrou
   for (int p = 0; p < (HAS_P1 ? 2 : 1); ++p) {
     ProbArgs& pa = a.prob[p];
     if (pa.dyn_role == 1) {
+      if (a.dyn.plan && rows > 0 && rows != a.dyn.chunk) {
+        const DhPlan c = *a.dyn.plan;
+        pa.wide_cols = c.wide_cols;
+        pa.k_splits = c.k_splits;
+        pa.k_cols = c.k_cols;
+        pa.raster.n_tiles = c.k_cols * c.k_splits;
+      }
       pa.raster = tile_raster(ceil_div64(rows, G::TILE_M), pa.raster.n_tiles, pa.dyn_bands_fastest != 0);
     } else if (given && (pa.dyn_role == 3 || pa.dyn_role == 4)) {
       if (rows == 0) pa.raster.num_units = 0;
@@ -146,24 +157,25 @@ __device__ __forceinline__ void apply_live_rows(GemmArgs& a, int rows, int ngrou
 }
 
 // Compile-time description of a problem: its epilogue, operand majorness,
-// the L2 eviction priority of each operand's loads (L2Hint), and whether its
-// units are wide.  A wide unit computes two neighbouring 256-column tiles of
+// the L2 eviction priority of each operand's loads (L2Hint), whether its units
+// are wide, and whether a tile's K blocks may be cut into ranges that separate
+// units compute (KSPLIT; the epilogue gets the range's index).  A wide unit computes two neighbouring 256-column tiles of
 // one band (column tiles 2n and 2n + 1 for raster column n) into the two
 // accumulators at once, so each K block's A tile is loaded once for both:
 // three quarters of the operand bytes per MMA block of a one-tile unit.  The
 // epilogue of a wide unit cannot overlap the next unit's MMAs, so wide units
 // suit problems whose tiles run many K blocks.
-template <class EpiT, bool AMN, bool BMN, int AH = kL2Normal, int BH = kL2Normal, bool W = false>
+template <class EpiT, bool AMN, bool BMN, int AH = kL2Normal, int BH = kL2Normal, bool W = false, bool KS = false>
 struct Prob {
   using Epi = EpiT;
-  static constexpr bool A_MN = AMN, B_MN = BMN, present = true, WIDE = W;
+  static constexpr bool A_MN = AMN, B_MN = BMN, present = true, WIDE = W, KSPLIT = KS;
   static constexpr int A_HINT = AH, B_HINT = BH;
 };
 
 struct EpiNone;
 struct NoProb {
   using Epi = EpiNone;
-  static constexpr bool A_MN = false, B_MN = false, present = false, WIDE = false;
+  static constexpr bool A_MN = false, B_MN = false, present = false, WIDE = false, KSPLIT = false;
   static constexpr int A_HINT = kL2Normal, B_HINT = kL2Normal;
 };
 
@@ -210,6 +222,7 @@ struct EpiCtx {
   bool issuer;
   uint32_t seq;
   int rows_valid;       // live rows of a DynRows launch, else -1
+  int part_row0;        // KSPLIT: rows of the K ranges before this one (whole bands)
 };
 
 // Writes one 128-byte segment per thread (its row) into the next staging
@@ -357,6 +370,21 @@ __device__ __forceinline__ void next_acc(RoleState& st) {
   if (st.acc == 0) st.acc_phase ^= 1u;
 }
 
+// K blocks [kb0, kb1) and K range of raster column n; n becomes the column within the range.
+template <class P>
+__device__ __forceinline__ int unit_krange(const ProbArgs& pa, int& n, int& kb0, int& kb1) {
+  kb0 = 0;
+  kb1 = pa.num_kb;
+  if constexpr (P::KSPLIT) {
+    const int part = n / pa.k_cols;
+    n -= part * pa.k_cols;
+    kb0 = (int)((int64_t)pa.num_kb * part / pa.k_splits);
+    kb1 = (int)((int64_t)pa.num_kb * (part + 1) / pa.k_splits);
+    return part;
+  }
+  return 0;
+}
+
 // Column tiles of raster column n: [first, first + count).
 template <class P>
 __device__ __forceinline__ void unit_cols(const ProbArgs& pa, int n, int& first, int& count) {
@@ -378,9 +406,10 @@ __device__ __forceinline__ bool produce_unit(const Smem<G>& L, RoleState& st, ui
   int m, split, n0, n1;
   decode_unit(pa.raster, u, m, split, n0, n1);
   for (int n = n0; n < n1; ++n) {
-    int c0, nc;
-    unit_cols<P>(pa, n, c0, nc);
-    for (int kb = 0; kb < pa.num_kb; ++kb) {
+    int c0, nc, kb0, kb1, col = n;
+    unit_krange<P>(pa, col, kb0, kb1);
+    unit_cols<P>(pa, col, c0, nc);
+    for (int kb = kb0; kb < kb1; ++kb) {
       // stage 1: A and the first column tile's B; stage 2 (wide units): the second B
       for (int h = 0; h < nc; ++h) {
         if (!mbar_wait_bounded(L.empty(st.stage), st.phase ^ 1u, L.abort_flag)) return false;
@@ -409,8 +438,9 @@ __device__ __forceinline__ bool mma_unit(const Smem<G>& L, RoleState& st, uint32
   int m, split, n0, n1;
   decode_unit(pa.raster, u, m, split, n0, n1);
   for (int n = n0; n < n1; ++n) {
-    int c0, nc;
-    unit_cols<P>(pa, n, c0, nc);
+    int c0, nc, kb0, kb1, col = n;
+    unit_krange<P>(pa, col, kb0, kb1);
+    unit_cols<P>(pa, col, c0, nc);
     // the unit's accumulators: this one and, for a wide unit, the next
     RoleState a2 = st;
     next_acc(a2);
@@ -418,7 +448,7 @@ __device__ __forceinline__ bool mma_unit(const Smem<G>& L, RoleState& st, uint32
     if (nc == 2 && !mbar_wait_bounded(L.tempty(a2.acc), a2.acc_phase ^ 1u, L.abort_flag)) return false;
     tc_fence_after();
     const uint32_t d0 = tmem_base + st.acc * BN, d1 = tmem_base + a2.acc * BN;
-    for (int kb = 0; kb < pa.num_kb; ++kb) {
+    for (int kb = kb0; kb < kb1; ++kb) {
       // stage 1 holds A and the first B, stage 2 (wide units) the second B
       RoleState s2 = st;
       next_stage<G>(s2);
@@ -430,7 +460,7 @@ __device__ __forceinline__ bool mma_unit(const Smem<G>& L, RoleState& st, uint32
       const uint32_t sb1 = L.sbase + s2.stage * G::STAGE_BYTES + G::A_BYTES;
 #pragma unroll
       for (int kk = 0; kk < BK / UMMA_K; ++kk) {
-        const uint32_t accum = (kb | kk) != 0 ? 1u : 0u;
+        const uint32_t accum = ((kb - kb0) | kk) != 0 ? 1u : 0u;
         const uint64_t da = operand_desc<P::A_MN>(sa, kk);
         if constexpr (PAIR) {
           tc_mma_bf16_pair(d0, da, operand_desc<P::B_MN>(sb0, kk), idesc, accum);
@@ -465,8 +495,9 @@ __device__ __forceinline__ bool epi_unit(const Smem<G>& L, RoleState& st, uint32
   cx.row_base = m * G::TILE_M + (int)rank * BM;
   epi.begin_unit(ep, grow, split, n0, cx);
   for (int n = n0; n < n1; ++n) {
-    int c0, nc;
-    unit_cols<P>(pa, n, c0, nc);
+    int c0, nc, kb0, kb1, col = n;
+    cx.part_row0 = unit_krange<P>(pa, col, kb0, kb1) * pa.raster.m_tiles * G::TILE_M;
+    unit_cols<P>(pa, col, c0, nc);
     for (int h = 0; h < nc; ++h) {      // a wide unit's two tiles, one accumulator each
       // One outcome for all 128 epilogue threads: tcgen05.ld needs whole
       // warps and the store path synchronises the four warps.
@@ -494,6 +525,7 @@ __device__ __forceinline__ EpiCtx make_epi_ctx(uint32_t staging) {
   cx.seq = 0;
   cx.row_base = 0;
   cx.rows_valid = -1;
+  cx.part_row0 = 0;
   return cx;
 }
 

@@ -144,6 +144,68 @@ KD_HD int64_t logp_part_slots(int64_t N) { return 16 * N + (int64_t)kLogpMaxSpli
 // slots above): 96 for one band, else ceil(rows / 256) * slots / rows.
 KD_HD int64_t logp_units_bound(int64_t N) { return kLogpMaxSplits + logp_part_slots(N) / 128; }
 
+// The dH product of a chunk of the label log-probabilities' gradient, beside
+// dW's U1 units of k1 K blocks.  A dH tile runs k0 = V / 64 K blocks (half a
+// millisecond at V = 128,256), so a few bands of rows leave most groups idle:
+// its K blocks are then cut into ranges, each a unit of its own, whose fp32
+// parts are added up afterwards in order.  Chosen is the cut, and wide units
+// or not (see wide_pays), with the least work of the busiest group, counting
+// for each range the parts' bytes, written and read again (8 a value; a K block
+// of a group, a quarter of a microsecond, is about 2^20 bytes of traffic).
+constexpr int kMaxDhSplits = 64;
+
+struct DhPlan {
+  int wide_cols;   // 256-column tiles when units are wide, else 0
+  int k_splits;    // K ranges
+  int k_cols;      // raster columns of one range
+};
+
+// Rows (of d floats) that hold the parts of a chunk of C rows: the ranges of
+// bands of 256 rows; a single band can be cut into all kMaxDhSplits.
+KD_HD int64_t dh_part_rows(int64_t C) { return ceil_div64(C, 256) * 256 + (int64_t)kMaxDhSplits * 256; }
+
+// Cost of k_splits ranges, wide units or not; < 0 when not possible.
+KD_HD int64_t dh_cost(int64_t bands, int64_t n_cols, int64_t d, int64_t k0, int64_t U1, int64_t k1, int groups,
+                      bool wide, int k_splits, int64_t part_rows) {
+  if (k_splits > kMaxDhSplits || k_splits > k0 || (k_splits > 1 && bands * 256 * k_splits > part_rows) ||
+      (wide && n_cols < 2))
+    return -1;
+  const int64_t avg = ceil_div64(bands * n_cols * k0 + U1 * k1, groups);
+  const int64_t units = bands * k_splits * (wide ? ceil_div64(n_cols, 2) : n_cols);
+  const int64_t own = ceil_div64(units, groups) * ceil_div64(k0, k_splits) * (wide ? 2 : 1);
+  return (own > avg ? own : avg) + ((k_splits * bands * 256 * d * 8) >> 20);
+}
+
+// Candidates in the order of preference: fewer ranges first, then wide units.
+KD_HD void dh_candidate(int i, bool& wide, int& k_splits) {
+  wide = i % 2 == 0;
+  k_splits = i / 2 + 1;
+}
+
+KD_HD DhPlan dh_plan_of(int i, int64_t n_cols) {
+  bool wide;
+  int k_splits;
+  dh_candidate(i, wide, k_splits);
+  return DhPlan{wide ? (int)n_cols : 0, k_splits, (int)(wide ? ceil_div64(n_cols, 2) : n_cols)};
+}
+
+KD_HD DhPlan dh_plan(int64_t bands, int64_t n_cols, int64_t d, int64_t k0, int64_t U1, int64_t k1, int groups,
+                     int64_t part_rows) {
+  int best = 1;
+  int64_t least = -1;
+  for (int i = 0; i < 2 * kMaxDhSplits; ++i) {
+    bool wide;
+    int ks;
+    dh_candidate(i, wide, ks);
+    const int64_t c = dh_cost(bands, n_cols, d, k0, U1, k1, groups, wide, ks, part_rows);
+    if (c >= 0 && (least < 0 || c < least)) {
+      least = c;
+      best = i;
+    }
+  }
+  return dh_plan_of(best, n_cols);
+}
+
 // Two problems in one launch.  Problem 0's U0 units (k0 K blocks each) go
 // round-robin over `groups`, so groups [0, r), r = U0 % groups, run one more
 // of them than the others.  Problem 1's U1 units (k1 K blocks each) are dealt

@@ -41,7 +41,7 @@ Layout make_layout(int64_t S) {
 
 int check_sequences(int64_t S, int64_t N, const void* offsets, int offsets_i64) {
   if (S < 0 || N < 0 || (offsets_i64 & ~1)) return KD_ERR_INVALID_ARG;
-  if (S >= (int64_t(1) << 31) || N >= (int64_t(1) << 40)) return KD_ERR_UNSUPPORTED;
+  if (S >= (int64_t(1) << 31) || N > kMaxTokens) return KD_ERR_UNSUPPORTED;
   if (!offsets && (S == 0 ? N != 0 : N % S != 0)) return KD_ERR_INVALID_ARG;
   if (offsets && !aligned(offsets, offsets_i64 ? 8 : 4)) return KD_ERR_INVALID_ARG;
   return KD_OK;
@@ -72,6 +72,11 @@ bool all_aligned16(std::initializer_list<const void*> ps) {
   for (const void* p : ps)
     if (p && !aligned(p, 16)) return false;
   return true;
+}
+
+void two_floats(double v, float* h, float* l) {
+  *h = (float)v;
+  *l = (float)(v - (double)*h);
 }
 
 int launched() { return cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA; }
@@ -177,9 +182,9 @@ int kd_policy_loss(const float* logp, const float* old_logp, const float* ref_lo
   A.per_sequence = per_sequence;
   A.kl_kind = kl_kind;
   A.dual = dual_clip != 0.0;
-  A.log_hi = std::log1p(clip_high);
-  A.log_lo = std::log1p(-clip_low);
-  A.log_dual = A.dual ? std::log(dual_clip) : 0.0;
+  two_floats(std::log1p(clip_high), &A.hi_h, &A.hi_l);
+  two_floats(std::log1p(-clip_low), &A.lo_h, &A.lo_l);
+  two_floats(A.dual ? std::log(dual_clip) : 0.0, &A.dual_h, &A.dual_l);
   A.hi = (float)clip_high;
   A.lo = (float)clip_low;
   A.dual_c = (float)dual_clip;
@@ -198,13 +203,14 @@ int kd_policy_loss(const float* logp, const float* old_logp, const float* ref_lo
 
 int kd_scale_gradient(const float* x, const float* g, float* out, int64_t N, void* stream) {
   if (N < 0 || !g || (N > 0 && (!x || !out))) return KD_ERR_INVALID_ARG;
+  if (N > kMaxTokens) return KD_ERR_UNSUPPORTED;
   if (!aligned(x, 4) || !aligned(g, 4) || !aligned(out, 4)) return KD_ERR_INVALID_ARG;
   if (N == 0) return KD_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t b = (N + kTokensPerItem - 1) / kTokensPerItem;
   const unsigned grid = (unsigned)(b < kLossBlocks ? b : kLossBlocks);
-  if (all_aligned16({x, out})) scale_kernel<true><<<grid, kThreads, 0, s>>>(x, g, out, N);
-  else scale_kernel<false><<<grid, kThreads, 0, s>>>(x, g, out, N);
+  if (all_aligned16({x, out})) scale_kernel<true><<<grid, kThreads, 0, s>>>(x, g, out, (int)N);
+  else scale_kernel<false><<<grid, kThreads, 0, s>>>(x, g, out, (int)N);
   return launched();
 }
 

@@ -24,10 +24,10 @@ namespace kd {
 namespace seq {
 
 constexpr int kThreads = 256;
-constexpr int kSumBlocks = 592;      // blocks of the first launch at most (4 per SM): partial totals to join
+constexpr int kSumBlocks = 1184;     // blocks of the first launch at most (8 per SM): partial totals to join
 constexpr int kLossBlocks = 4736;    // blocks of the second launch at most (32 per SM, several of them in turn)
-constexpr int kSumUnroll = 4;        // groups of four tokens whose loads a thread has in flight, first launch
-constexpr int kLossUnroll = 2;       // and second
+constexpr int kSumUnroll = 2;        // groups of four tokens whose loads a thread of the first launch has in flight
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - (int64_t(1) << 16);   // token indices fit an int, a stride past the end too
 
 // The sequences of an array of N tokens: sequence s is [offsets[s],
 // offsets[s + 1]), or row s of S rows of L tokens when offsets is null.
@@ -40,24 +40,24 @@ struct Sequences {
   int splits;          // items per sequence
 };
 
-__device__ __forceinline__ int64_t seq_offset(const Sequences& q, int64_t s) {
-  if (!q.offsets) return s * q.L;
+__device__ __forceinline__ int seq_offset(const Sequences& q, int64_t s) {
+  if (!q.offsets) return (int)(s * q.L);
   int64_t o = q.offsets_i64 ? static_cast<const int64_t*>(q.offsets)[s]
                             : (int64_t)static_cast<const int32_t*>(q.offsets)[s];
-  return o < 0 ? 0 : (o > q.N ? q.N : o);
+  return (int)(o < 0 ? 0 : (o > q.N ? q.N : o));
 }
 
 // Tokens [lo, hi) of item k of sequence s.
-__device__ __forceinline__ void item_range(const Sequences& q, int64_t s, int k, int64_t& lo, int64_t& hi) {
-  const int64_t b = seq_offset(q, s), e = seq_offset(q, s + 1);
+__device__ __forceinline__ void item_range(const Sequences& q, int64_t s, int k, int& lo, int& hi) {
+  const int b = seq_offset(q, s), e = seq_offset(q, s + 1);
   lo = b;
   hi = e;
   if (q.splits > 1) {
-    const int64_t a = b & ~int64_t(3);
-    const int64_t per = e > b ? ((e - a + q.splits - 1) / q.splits + 3) & ~int64_t(3) : 0;
-    const int64_t start = a + k * per;
-    if (start > lo) lo = start;
-    if (start + per < hi) hi = start + per;
+    const int a = b & ~3;
+    const int per = e > b ? ((e - a + q.splits - 1) / q.splits + 3) & ~3 : 0;
+    const int64_t start = a + (int64_t)k * per;        // past hi for the last ranges of a short sequence
+    if (start > lo) lo = start < hi ? (int)start : hi;
+    if (start + per < hi) hi = (int)(start + per);
   }
   if (hi < lo) hi = lo;
 }
@@ -65,7 +65,7 @@ __device__ __forceinline__ void item_range(const Sequences& q, int64_t s, int k,
 // Four tokens of an array from t0 (a multiple of 4): those of [lo, hi), zeros
 // for the others.
 template <bool VEC>
-__device__ __forceinline__ void load4(const float* __restrict__ p, int64_t t0, int64_t lo, int64_t hi, float (&v)[4]) {
+__device__ __forceinline__ void load4(const float* __restrict__ p, int t0, int lo, int hi, float (&v)[4]) {
   if (VEC && t0 >= lo && t0 + 4 <= hi) {
     const float4 f = *reinterpret_cast<const float4*>(p + t0);
     v[0] = f.x;
@@ -79,7 +79,7 @@ __device__ __forceinline__ void load4(const float* __restrict__ p, int64_t t0, i
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store4(float* __restrict__ p, int64_t t0, int64_t lo, int64_t hi, const float (&v)[4]) {
+__device__ __forceinline__ void store4(float* __restrict__ p, int t0, int lo, int hi, const float (&v)[4]) {
   if (VEC && t0 >= lo && t0 + 4 <= hi) {
     *reinterpret_cast<float4*>(p + t0) = make_float4(v[0], v[1], v[2], v[3]);
   } else {
@@ -91,7 +91,7 @@ __device__ __forceinline__ void store4(float* __restrict__ p, int64_t t0, int64_
 
 // The four tokens' weights: the mask, or one, inside [lo, hi); 0 outside.
 template <bool VEC>
-__device__ __forceinline__ void load_mask4(const float* __restrict__ mask, int64_t t0, int64_t lo, int64_t hi,
+__device__ __forceinline__ void load_mask4(const float* __restrict__ mask, int t0, int lo, int hi,
                                            float (&m)[4]) {
   if (mask) {
     load4<VEC>(mask, t0, lo, hi, m);
@@ -145,7 +145,7 @@ __device__ __forceinline__ bool last_block(unsigned int* counter) {
 // Tokens in no sequence (before the first, behind the last) have no gradient.
 __device__ __forceinline__ void zero_outside(const Sequences& q, float* __restrict__ out) {
   if (!q.offsets) return;
-  const int64_t b = seq_offset(q, 0), e = seq_offset(q, q.S);
+  const int b = seq_offset(q, 0), e = seq_offset(q, q.S);
   const int64_t step = (int64_t)gridDim.x * blockDim.x, i0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   for (int64_t t = i0; t < b; t += step) out[t] = 0.f;
   for (int64_t t = e + i0; t < q.N; t += step) out[t] = 0.f;
@@ -179,7 +179,7 @@ struct PrefArgs {
 };
 
 template <int TEAM, bool VEC>
-__global__ void __launch_bounds__(kThreads) pref_sums_kernel(const PrefArgs A) {
+__global__ void __launch_bounds__(kThreads, 4) pref_sums_kernel(const PrefArgs A) {
   __shared__ double red[kThreads / 32];
   if (blockIdx.x == 0 && threadIdx.x == 0) *A.counter = 0u;
   constexpr int kTeams = kThreads / TEAM;
@@ -187,14 +187,14 @@ __global__ void __launch_bounds__(kThreads) pref_sums_kernel(const PrefArgs A) {
   const int64_t items = A.q.S * A.q.splits;
   for (int64_t it = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; it < items; it += (int64_t)gridDim.x * kTeams) {
     const int64_t s = it / A.q.splits;
-    int64_t lo, hi;
+    int lo, hi;
     item_range(A.q, s, (int)(it - s * A.q.splits), lo, hi);
     double r = 0.0, n = 0.0;
-    for (int64_t t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM * kSumUnroll) {
+    for (int t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM * kSumUnroll) {
       float m[kSumUnroll][4], lp[kSumUnroll][4], rf[kSumUnroll][4];
 #pragma unroll
       for (int u = 0; u < kSumUnroll; ++u) {
-        const int64_t t = t0 + 4 * TEAM * u;
+        const int t = t0 + 4 * TEAM * u;
         load_mask4<VEC>(A.mask, t, lo, hi, m[u]);
         load4<VEC>(A.logp, t, lo, hi, lp[u]);
         if (A.ref) load4<VEC>(A.ref, t, lo, hi, rf[u]);
@@ -232,7 +232,7 @@ __device__ __forceinline__ void seq_ratio(const PrefArgs& A, int64_t s, double& 
 __device__ __forceinline__ double softplus64(double v) { return (v > 0.0 ? v : 0.0) + log1p(exp(-fabs(v))); }
 
 template <int TEAM, bool VEC>
-__global__ void __launch_bounds__(kThreads) pref_loss_kernel(const PrefArgs A) {
+__global__ void __launch_bounds__(kThreads, 4) pref_loss_kernel(const PrefArgs A) {
   __shared__ double red[kThreads / 32];
   __shared__ float s_coef;
   constexpr int kTeams = kThreads / TEAM;
@@ -280,15 +280,15 @@ __global__ void __launch_bounds__(kThreads) pref_loss_kernel(const PrefArgs A) {
       coef = s_coef;
       __syncthreads();
     }
-    int64_t lo, hi;
+    int lo, hi;
     item_range(A.q, s, k, lo, hi);
-    for (int64_t t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM * kSumUnroll) {
+    for (int t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM * kSumUnroll) {
       float m[kSumUnroll][4];
 #pragma unroll
       for (int u = 0; u < kSumUnroll; ++u) load_mask4<VEC>(A.mask, t0 + 4 * TEAM * u, lo, hi, m[u]);
 #pragma unroll
       for (int u = 0; u < kSumUnroll; ++u) {
-        const int64_t t = t0 + 4 * TEAM * u;
+        const int t = t0 + 4 * TEAM * u;
         float d[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) d[j] = m[u][j] != 0.f ? coef * m[u][j] : 0.f;
@@ -320,11 +320,13 @@ __global__ void __launch_bounds__(kThreads) pref_loss_kernel(const PrefArgs A) {
 //   dlogp = g w ( [not clipped] (-A r) + kl_coef (1 | y | 1 - e^-y) )
 // treats old, ref and A as constants.
 //
-// Whether a token is clipped is decided in 64 bits, x against log(1 + hi),
-// log(1 - lo) and log c: a difference of two floats is exact there, so the
-// decision is that of the formula and not of a rounded exponential.  e^x and
+// Whether a token is clipped is decided on the exact difference x, against
+// log(1 + hi), log(1 - lo) and log c: x as a float and the float it was rounded
+// by, the border as a float and the rest of it (see above_border).  So the
+// decision is the formula's and not that of a rounded exponential.  e^x and
 // the KL term are taken in 32 bits; e^-y - 1 + y, which cancels for small y,
-// by its series for |y| < 1/2.
+// by its series for |y| < 1/2.  Tokens are computed without branches, masked
+// ones on zeros: four at a time in flight instead of one behind the other.
 
 enum { kK1 = 0, kK2 = 1, kK3 = 2 };
 
@@ -332,7 +334,7 @@ struct PolicyArgs {
   Sequences q;
   const float *logp, *old, *ref, *adv, *mask, *grad_loss;
   int adv_per_seq, per_sequence, kl_kind, dual;
-  double log_hi, log_lo, log_dual;
+  float hi_h, hi_l, lo_h, lo_l, dual_h, dual_l;     // log borders, in two floats each
   float hi, lo, dual_c, kl_coef;
   double* sums;            // [S * splits] sum m
   double* total;           // [kSumBlocks] the first launch's blocks' sums
@@ -343,7 +345,7 @@ struct PolicyArgs {
 };
 
 template <int TEAM, bool VEC>
-__global__ void __launch_bounds__(kThreads) policy_sums_kernel(const PolicyArgs A) {
+__global__ void __launch_bounds__(kThreads, 8) policy_sums_kernel(const PolicyArgs A) {
   __shared__ double red[kThreads / 32];
   if (blockIdx.x == 0 && threadIdx.x == 0) *A.counter = 0u;
   constexpr int kTeams = kThreads / TEAM;
@@ -352,11 +354,11 @@ __global__ void __launch_bounds__(kThreads) policy_sums_kernel(const PolicyArgs 
   double all = 0.0;
   for (int64_t it = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; it < items; it += (int64_t)gridDim.x * kTeams) {
     const int64_t s = it / A.q.splits;
-    int64_t lo, hi;
+    int lo, hi;
     item_range(A.q, s, (int)(it - s * A.q.splits), lo, hi);
     double n = 0.0;
     if (A.mask) {
-      for (int64_t t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM * kSumUnroll) {
+      for (int t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM * kSumUnroll) {
         float m[kSumUnroll][4];
 #pragma unroll
         for (int u = 0; u < kSumUnroll; ++u) load4<VEC>(A.mask, t0 + 4 * TEAM * u, lo, hi, m[u]);
@@ -390,27 +392,24 @@ __device__ __forceinline__ float exp_tail_series(float x) {
   return fmaf(p, x, 0.5f);
 }
 
+// Sign of (x + rest) - (h + l): x - h is exact near the border, and far from it the rests decide nothing.
+__device__ __forceinline__ float above_border(float x, float rest, float h, float l) {
+  return __fadd_rn(__fsub_rn(x, h), __fsub_rn(rest, l));
+}
+
 // One token: its loss, KL estimate, whether it is clipped, and d loss / d logp.
 __device__ __forceinline__ void policy_token(const PolicyArgs& A, float lp, float old, float ref, float a, float& loss,
                                              float& kl, float& clipped, float& d) {
-  const double x = (double)lp - (double)old;
-  const float r = expf((float)x);
-  float obj = a == 0.f ? 0.f : r * a;         // A = 0: no term, whatever the ratio
-  float grad = -obj;
-  clipped = 0.f;
-  if (a > 0.f && x > A.log_hi) {
-    obj = (1.f + A.hi) * a;
-    grad = 0.f;
-    clipped = 1.f;
-  } else if (a < 0.f && x < A.log_lo) {
-    obj = (1.f - A.lo) * a;
-    grad = 0.f;
-    clipped = 1.f;
-  } else if (A.dual && a < 0.f && x > A.log_dual) {
-    obj = A.dual_c * a;
-    grad = 0.f;
-    clipped = 1.f;
-  }
+  const float x = __fsub_rn(lp, old), b = __fsub_rn(x, lp);
+  float rest = __fsub_rn(__fsub_rn(lp, __fsub_rn(x, b)), __fadd_rn(old, b));    // lp - old - x, exactly
+  rest = fabsf(x) < INFINITY ? rest : 0.f;
+  const bool over = above_border(x, rest, A.hi_h, A.hi_l) > 0.f, under = above_border(x, rest, A.lo_h, A.lo_l) < 0.f;
+  const bool far = A.dual && above_border(x, rest, A.dual_h, A.dual_l) > 0.f;
+  const bool clip = (a > 0.f && over) || (a < 0.f && (under || far));
+  const float border = a > 0.f ? 1.f + A.hi : (under ? 1.f - A.lo : A.dual_c);
+  const float ra = a == 0.f ? 0.f : expf(x) * a;      // A = 0: no term, whatever the ratio
+  const float obj = clip ? border * a : ra;
+  clipped = clip ? 1.f : 0.f;
   kl = 0.f;
   float dk = 0.f;
   if (A.ref) {
@@ -421,21 +420,19 @@ __device__ __forceinline__ void policy_token(const PolicyArgs& A, float lp, floa
     } else if (A.kl_kind == kK2) {
       kl = 0.5f * y * y;
       dk = y;
-    } else if (fabsf(y) < 0.5f) {
-      kl = y * y * exp_tail_series(-y);       // e^-y - 1 + y
-      dk = y - kl;                            // 1 - e^-y
     } else {
       const float e = expf(-y);
-      kl = e - 1.f + y;
-      dk = 1.f - e;
+      const bool small = fabsf(y) < 0.5f;
+      kl = small ? y * y * exp_tail_series(-y) : e - 1.f + y;      // e^-y - 1 + y
+      dk = small ? y - kl : 1.f - e;                               // 1 - e^-y
     }
   }
   loss = fmaf(A.kl_coef, kl, -obj);
-  d = fmaf(A.kl_coef, dk, grad);
+  d = fmaf(A.kl_coef, dk, clip ? 0.f : -ra);
 }
 
 template <int TEAM, bool VEC>
-__global__ void __launch_bounds__(kThreads) policy_loss_kernel(const PolicyArgs A) {
+__global__ void __launch_bounds__(kThreads, 4) policy_loss_kernel(const PolicyArgs A) {
   __shared__ double red[kThreads / 32];
   constexpr int kTeams = kThreads / TEAM;
   const int tid = threadIdx.x % TEAM;
@@ -451,7 +448,7 @@ __global__ void __launch_bounds__(kThreads) policy_loss_kernel(const PolicyArgs 
   double sum_l = 0.0, sum_k = 0.0, sum_c = 0.0;
   for (int64_t it = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; it < items; it += (int64_t)gridDim.x * kTeams) {
     const int64_t s = it / A.q.splits;
-    int64_t lo, hi;
+    int lo, hi;
     item_range(A.q, s, (int)(it - s * A.q.splits), lo, hi);
     double w = inv_total;
     if (A.per_sequence) {
@@ -461,41 +458,29 @@ __global__ void __launch_bounds__(kThreads) policy_loss_kernel(const PolicyArgs 
     const float wg = (float)w * g;
     const float as = A.adv_per_seq ? A.adv[s] : 0.f;
     double il = 0.0, ik = 0.0, ic = 0.0;
-    for (int64_t t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM * kLossUnroll) {
-      float m[kLossUnroll][4], lp[kLossUnroll][4], od[kLossUnroll][4], rf[kLossUnroll][4], a[kLossUnroll][4];
+    float next[4];                            // the next group's mask, loaded a group ahead
+    load_mask4<VEC>(A.mask, ((lo >> 2) + tid) << 2, lo, hi, next);
+    for (int t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM) {
+      float m[4] = {next[0], next[1], next[2], next[3]}, d[4] = {0.f, 0.f, 0.f, 0.f};
+      load_mask4<VEC>(A.mask, t0 + 4 * TEAM, lo, hi, next);
+      if (m[0] != 0.f || m[1] != 0.f || m[2] != 0.f || m[3] != 0.f) {     // padding costs its mask alone
+        float lp[4], od[4], rf[4], a[4], l[4], k[4], c[4];
+        load4<VEC>(A.logp, t0, lo, hi, lp);
+        load4<VEC>(A.old, t0, lo, hi, od);
+        if (A.ref) load4<VEC>(A.ref, t0, lo, hi, rf);
+        if (!A.adv_per_seq) load4<VEC>(A.adv, t0, lo, hi, a);
 #pragma unroll
-      for (int u = 0; u < kLossUnroll; ++u) load_mask4<VEC>(A.mask, t0 + 4 * TEAM * u, lo, hi, m[u]);
-#pragma unroll
-      for (int u = 0; u < kLossUnroll; ++u) {
-        const int64_t t = t0 + 4 * TEAM * u;
-        if (m[u][0] != 0.f || m[u][1] != 0.f || m[u][2] != 0.f || m[u][3] != 0.f) {   // padding costs its mask alone
-          load4<VEC>(A.logp, t, lo, hi, lp[u]);
-          load4<VEC>(A.old, t, lo, hi, od[u]);
-          if (A.ref) load4<VEC>(A.ref, t, lo, hi, rf[u]);
-          if (!A.adv_per_seq) load4<VEC>(A.adv, t, lo, hi, a[u]);
+        for (int j = 0; j < 4; ++j) {         // a masked place may hold anything, NaN included
+          const bool on = m[j] != 0.f;
+          policy_token(A, on ? lp[j] : 0.f, on ? od[j] : 0.f, on && A.ref ? rf[j] : 0.f,
+                       on ? (A.adv_per_seq ? as : a[j]) : 0.f, l[j], k[j], c[j], d[j]);
+          d[j] = on ? wg * m[j] * d[j] : 0.f;
         }
+        il += (double)fmaf(m[0], l[0], fmaf(m[1], l[1], fmaf(m[2], l[2], m[3] * l[3])));
+        ik += (double)fmaf(m[0], k[0], fmaf(m[1], k[1], fmaf(m[2], k[2], m[3] * k[3])));
+        ic += (double)fmaf(m[0], c[0], fmaf(m[1], c[1], fmaf(m[2], c[2], m[3] * c[3])));
       }
-#pragma unroll
-      for (int u = 0; u < kLossUnroll; ++u) {
-        const int64_t t = t0 + 4 * TEAM * u;
-        float d[4], l4 = 0.f, k4 = 0.f, c4 = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          d[j] = 0.f;
-          if (m[u][j] != 0.f) {               // a masked place may hold anything, NaN included
-            float l, k, c, dd;
-            policy_token(A, lp[u][j], od[u][j], rf[u][j], A.adv_per_seq ? as : a[u][j], l, k, c, dd);
-            l4 = fmaf(m[u][j], l, l4);
-            k4 = fmaf(m[u][j], k, k4);
-            c4 = fmaf(m[u][j], c, c4);
-            d[j] = wg * m[u][j] * dd;
-          }
-        }
-        il += (double)l4;
-        ik += (double)k4;
-        ic += (double)c4;
-        if (A.dlogp && t < hi) store4<VEC>(A.dlogp, t, lo, hi, d);
-      }
+      if (A.dlogp) store4<VEC>(A.dlogp, t0, lo, hi, d);
     }
     sum_l += w != 0.0 ? w * il : 0.0;
     sum_k += w != 0.0 ? w * ik : 0.0;
@@ -526,14 +511,14 @@ __global__ void __launch_bounds__(kThreads) policy_loss_kernel(const PolicyArgs 
 // out = x g, the gradient of a loss whose unit gradient x was kept.
 template <bool VEC>
 __global__ void __launch_bounds__(kThreads) scale_kernel(const float* __restrict__ x, const float* __restrict__ g,
-                                                         float* __restrict__ out, int64_t n) {
+                                                         float* __restrict__ out, int n) {
   const float s = *g;
   for (int64_t t0 = 4 * ((int64_t)blockIdx.x * kThreads + threadIdx.x); t0 < n; t0 += 4 * (int64_t)gridDim.x * kThreads) {
     float v[4];
-    load4<VEC>(x, t0, 0, n, v);
+    load4<VEC>(x, (int)t0, 0, n, v);
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] *= s;
-    store4<VEC>(out, t0, 0, n, v);
+    store4<VEC>(out, (int)t0, 0, n, v);
   }
 }
 

@@ -38,6 +38,7 @@ struct LiveRows {
   int count;         // rows that take part
   int pad;
   Raster raster;     // forward: of all of them; backward: of the last, partly filled chunk
+  DhPlan dh;         // backward: how that chunk's dH product is cut
 };
 
 struct LabelPrep {
@@ -55,6 +56,9 @@ struct LabelPrep {
   int64_t part_slots;             // forward: bounds the ranges by the partial slots (0: no bound)
   int64_t band_bytes, l2_bytes;
   unsigned int* wave;             // forward: pacing counters to clear
+  // backward: the joint launch of dH and dW (see dh_plan)
+  int64_t d, dw_units, part_rows;
+  int joint_groups;
 };
 
 // One block lists the tokens that take part, in increasing order, with their
@@ -63,11 +67,11 @@ struct LabelPrep {
 __global__ void __launch_bounds__(kLabelThreads) label_prep_kernel(const LabelPrep P) {
   __shared__ int s_warp[kLabelThreads / 32];
   __shared__ unsigned int s_bad;
-  __shared__ unsigned long long s_best;
+  __shared__ unsigned long long s_best, s_dh;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   if (t == 0) {
     s_bad = 0u;
-    s_best = ~0ull;
+    s_best = s_dh = ~0ull;
   }
   int total = 0;
   for (int64_t base = 0; base < P.N; base += 4 * kLabelThreads) {
@@ -131,6 +135,15 @@ __global__ void __launch_bounds__(kLabelThreads) label_prep_kernel(const LabelPr
   __syncthreads();
   if (rows > 0 && t + 1 <= most && t + 1 <= P.n_tiles)
     atomicMin(&s_best, ((unsigned long long)split_cost(m_tiles, P.n_tiles, P.groups, t + 1) << 32) | (unsigned)(t + 1));
+  const int64_t n_cols = ceil_div64(P.d, 256);
+  if (P.chunk > 0 && rows > 0 && t < 2 * kMaxDhSplits) {
+    bool wide;
+    int ks;
+    dh_candidate(t, wide, ks);
+    const int64_t c = dh_cost(m_tiles, n_cols, P.d, ceil_div64(P.V, BK), P.dw_units, ceil_div64(rows, BK),
+                              P.joint_groups, wide, ks, P.part_rows);
+    if (c >= 0) atomicMin(&s_dh, ((unsigned long long)c << 32) | (unsigned)t);
+  }
   __syncthreads();
   Raster r{};
   if (rows > 0)
@@ -138,6 +151,7 @@ __global__ void __launch_bounds__(kLabelThreads) label_prep_kernel(const LabelPr
   if (t == 0) {
     P.live->count = total;
     P.live->raster = r;
+    if (P.chunk > 0 && rows > 0) P.live->dh = dh_plan_of((int)(unsigned)s_dh, n_cols);
     P.status->bad_index = s_bad;
     P.status->timeout = 0u;
   }
@@ -437,6 +451,55 @@ struct EpiDlogp {
     }
   }
 };
+
+// dH of a chunk's live rows, or the part of it that one K range gives: fp32
+// rows of the parts' buffer (`out`: box {32, 128}, 128-byte swizzle).
+struct EpiDhPart {
+  static constexpr bool kStaging = true;
+  struct Params {
+    int unused;
+  };
+  __device__ __forceinline__ void begin_unit(const Params&, int, int, int, const EpiCtx&) {}
+  __device__ __forceinline__ void end_unit(const Params&, int, int) {}
+
+  __device__ __forceinline__ void tile(const Params&, const CUtensorMap* out, int, int n, uint32_t taddr, EpiCtx& cx) {
+#pragma unroll 1
+    for (int j = 0; j < BN / 32; ++j) {
+      float v[32];
+      __syncwarp();
+      tmem_ld_32x32b_x32(taddr + j * 32, v);
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+      stage_store(cx, out, n * BN + j * 32, cx.part_row0 + cx.row_base, w, false);
+    }
+  }
+};
+
+// dH[token] = bf16(sum over the K ranges, in order) for the chunk's live rows;
+// eight values a thread.  `full` is the plan of a chunk that is live throughout.
+__global__ void __launch_bounds__(256)
+dh_finish_kernel(const float4* __restrict__ part, int d8, const int32_t* __restrict__ rowmap,
+                 const LiveRows* __restrict__ live, int row0, int C, int full_splits, uint4* __restrict__ dH) {
+  int rows = live->count - row0;
+  rows = rows < 0 ? 0 : (rows > C ? C : rows);
+  const int splits = rows == C ? full_splits : live->dh.k_splits;
+  const size_t stride = (size_t)ceil_div64(rows, 256) * 256 * d8 * 2;
+  const int64_t total = (int64_t)rows * d8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int r = (int)(i / d8), j = (int)(i - (int64_t)r * d8);
+    const float4* p = part + ((size_t)r * d8 + j) * 2;
+    float4 a = p[0], b = p[1];
+#pragma unroll 4
+    for (int k = 1; k < splits; ++k) {
+      const float4 x = p[k * stride], y = p[k * stride + 1];
+      a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+      b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
+    }
+    dH[(size_t)rowmap[row0 + r] * d8 + j] =
+        make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+  }
+}
 
 // dW = dZ^T H of a single chunk, rounded to bf16 and stored (`out`: dW [V][d]
 // bf16, box {64, 128}, 128-byte swizzle): half the bytes of an fp32 dW, and

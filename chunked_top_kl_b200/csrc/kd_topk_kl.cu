@@ -9,8 +9,8 @@
 //                      (bracketed steps: skipping masked rows)
 // Label log-probabilities: label_prep -> gather_live -> gemm<EpiLogp> ->
 //                      logp_merge; gradient: label_prep -> for each chunk,
-//                      gather_live -> gemm<EpiDlogp> -> gemm<EpiDh + EpiDw or
-//                      EpiDwHalf> -> scatter_rows
+//                      gather_live -> gemm<EpiDlogp> -> gemm<EpiDhPart + EpiDw
+//                      or EpiDwHalf> -> dh_finish
 // Teacher top-K cache writer: for each chunk, gemm<EpiZ32> (fp32 logits and
 //                      their tile maxima) -> topk_select
 // The fused chunked loss of "Efficient Knowledge Distillation for LLMs"
@@ -844,6 +844,7 @@ int kd_teacher_topk(const void* Ht, const void* Wt, int64_t N, int64_t d, int64_
 
 namespace {
 
+using ProbDhPart = Prob<EpiDhPart, false, true, kL2Normal, kL2Normal, true, true>;   // ProbDh, its K cut where rows are few
 using ProbDwHalf = Prob<EpiDwHalf, true, true, kL2Normal, kL2EvictLast>;   // ProbDw with a bf16 result
 template <bool ENT>
 using ProbLogp = Prob<EpiLogp<ENT>, false, false, kL2EvictLast, kL2Normal>;
@@ -853,8 +854,8 @@ using ProbDlogp = Prob<EpiDlogp<ENT>, false, false, kL2EvictLast, kL2Normal>;
 struct LogpLayout {
   size_t off_status = 0, off_live = 0, off_rowmap = 0, off_lab = 0;
   size_t off_part = 0, off_wave = 0, off_zlab = 0, off_hc = 0;         // forward
-  size_t off_jwave = 0, off_dz = 0, off_dhc = 0, off_dw32 = 0;         // backward
-  int64_t slots = 0, C = 0, ldz = 0, jwave_per_chunk = 0;
+  size_t off_jwave = 0, off_dz = 0, off_part32 = 0, off_dw32 = 0;      // backward
+  int64_t slots = 0, C = 0, ldz = 0, jwave_per_chunk = 0, part_rows = 0;
   size_t total = 0;
 };
 
@@ -877,12 +878,12 @@ LogpLayout make_logp_layout(int64_t N, int64_t d, int64_t V, int64_t chunk, bool
   } else {
     L.C = chunk < n ? chunk : n;
     L.ldz = round_up(V, 8);
-    L.jwave_per_chunk =
-        wave_slots_bound(ceil_div(L.C, 256) * ceil_div(d, 256), ceil_div(V, 256) * ceil_div(d, 256));
+    L.part_rows = dh_part_rows(L.C);
+    L.jwave_per_chunk = wave_slots_bound(L.part_rows / 256 * ceil_div(d, 256), ceil_div(V, 256) * ceil_div(d, 256));
     L.off_jwave = take(sizeof(unsigned int) * (size_t)L.jwave_per_chunk * ceil_div(n, L.C));
     L.off_dz = take(2 * (size_t)L.C * L.ldz);
     L.off_hc = take(2 * (size_t)(L.C > kPadRows ? L.C : kPadRows) * d);
-    L.off_dhc = take(2 * (size_t)L.C * d);
+    L.off_part32 = take(sizeof(float) * (size_t)L.part_rows * d);
     if (half_dW && n > L.C) L.off_dw32 = take(sizeof(float) * (size_t)V * d);
   }
   L.total = o;
@@ -973,16 +974,21 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
   lp.n_tiles = (int)n_tiles;
   lp.groups = dz_groups;
   lp.max_splits = kMaxDzSplits;
+  const bool with_dW = dW != nullptr, rounds = half_dW && N > C;        // several chunks add up in fp32 first
+  const int64_t dh_cols = ceil_div(d, BN), dw_units = with_dW ? ceil_div(V, GeoP::TILE_M) * dh_cols : 0;
+  lp.d = d;
+  lp.dw_units = dw_units;
+  lp.part_rows = L.part_rows;
+  lp.joint_groups = groups;
   if (cudaMemsetAsync(dH, 0, sizeof(__nv_bfloat16) * (size_t)N * d, s) != cudaSuccess) return KD_ERR_CUDA;
   label_prep_kernel<<<1, kLabelThreads, 0, s>>>(lp);
   if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
 
-  const bool with_dW = dW != nullptr, rounds = half_dW && N > C;        // several chunks add up in fp32 first
   void* dWacc = rounds ? static_cast<void*>(at<float>(ws, L.off_dw32)) : dW;
   const bool half_store = half_dW && !rounds;
   __nv_bfloat16* dz = at<__nv_bfloat16>(ws, L.off_dz);
   void* hc = at<char>(ws, L.off_hc);
-  void* dhc = at<char>(ws, L.off_dhc);
+  float* part32 = at<float>(ws, L.off_part32);
   unsigned int* jwave = at<unsigned int>(ws, L.off_jwave);
   if (with_dW && cudaMemsetAsync(jwave, 0, sizeof(unsigned int) * (size_t)L.jwave_per_chunk * ceil_div(N, C), s) !=
                      cudaSuccess)
@@ -990,7 +996,7 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
   CUtensorMap tmHk, tmWk, tmWmn, tmHmn, tmDH, tmDW;
   if (!make_map(&tmHk, hc, d, C, d, BK, BM) || !make_map(&tmWk, W, d, V, d, BK, GeoP::B_ROWS) ||
       !make_map(&tmWmn, W, d, V, d, 64, BK) || !make_map(&tmHmn, hc, d, C, d, 64, BK) ||
-      !make_map(&tmDH, dhc, d, C, d, 64, BM))
+      !make_map(&tmDH, part32, d, L.part_rows, d, 32, BM, true))
     return KD_ERR_CUDA;
   if (with_dW && !(half_store ? make_map(&tmDW, dWacc, d, V, d, 64, BM) : make_map(&tmDW, dWacc, d, V, d, 32, BM, true)))
     return KD_ERR_CUDA;
@@ -1001,7 +1007,7 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
     CUtensorMap tmZk, tmZmn;
     if (!make_map(&tmZk, dz, L.ldz, Cc, L.ldz, BK, BM) || !make_map(&tmZmn, dz, L.ldz, Cc, L.ldz, 64, BK))
       return KD_ERR_CUDA;
-    const DynRows dyn{&live->count, (int)c0, (int)Cc, &live->raster};
+    const DynRows dyn{&live->count, (int)c0, (int)Cc, &live->raster, &live->dh};
     const int64_t want = ceil_div(Cc, 8);
     const unsigned blocks = (unsigned)(want < copy_blocks ? want : copy_blocks);
     gather_live_kernel<<<blocks, 256, 0, s>>>(static_cast<const uint4*>(H), (int)(d / 8), lp.rowmap, live, (int)c0,
@@ -1031,40 +1037,42 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
     GemmArgs j{};
     j.status = lp.status;
     j.dyn = dyn;
-    const int64_t dh_cols = ceil_div(d, BN), dh_bands = ceil_div(Cc, GeoP::TILE_M);
-    const int64_t dw_units = with_dW ? ceil_div(V, GeoP::TILE_M) * dh_cols : 0;
-    const bool wide = wide_pays(dh_bands, dh_cols, ceil_div(V, BK), dw_units, ceil_div(Cc, BK), groups);
-    j.prob[0].raster = tile_raster(dh_bands, wide ? ceil_div(dh_cols, 2) : dh_cols, false);
+    const int64_t dh_bands = ceil_div(Cc, GeoP::TILE_M), k1 = with_dW ? ceil_div(Cc, BK) : 0;
+    const DhPlan plan = dh_plan(dh_bands, dh_cols, d, ceil_div(V, BK), dw_units, k1, groups, L.part_rows);
+    j.prob[0].raster = tile_raster(dh_bands, (int64_t)plan.k_cols * plan.k_splits, false);
     j.prob[0].num_kb = (int)ceil_div(V, BK);
     j.prob[0].dyn_role = 1;
-    j.prob[0].wide_cols = wide ? (int)dh_cols : 0;
-    EpiDh::Params eh{};
-    eh.row0 = 0;
+    j.prob[0].wide_cols = plan.wide_cols;
+    j.prob[0].k_splits = plan.k_splits;
+    j.prob[0].k_cols = plan.k_cols;
+    EpiDhPart::Params eh{};
     cudaError_t e;
     if (!with_dW) {
       EpiNone::Params none{};
-      e = launch_gemm<ProbDh, NoProb, kPair>(9, dev, groups, tmZk, tmWmn, tmDH, tmZk, tmWmn, tmDH, j, eh, none, s);
+      e = launch_gemm<ProbDhPart, NoProb, kPair>(9, dev, groups, tmZk, tmWmn, tmDH, tmZk, tmWmn, tmDH, j, eh, none, s);
     } else {
       j.prob[1].raster = tile_raster(ceil_div(V, GeoP::TILE_M), dh_cols, false);
       j.prob[1].num_kb = (int)ceil_div(Cc, BK);
       j.prob[1].dyn_role = 2;
       plan_second_problem(j, groups);
-      if (j.prob[1].num_kb >= (wide ? kPaceKBlocksWide : kPaceKBlocks))
+      if (j.prob[1].num_kb >= (plan.wide_cols ? kPaceKBlocksWide : kPaceKBlocks))
         j.wave_sync = jwave + (size_t)(c0 / C) * L.jwave_per_chunk;
       if (half_store) {
         j.prob[1].dyn_zero_fill = 1;
         EpiDwHalf::Params eb{};
-        e = launch_gemm<ProbDh, ProbDwHalf, kPair>(8, dev, groups, tmZk, tmWmn, tmDH, tmZmn, tmHmn, tmDW, j, eh, eb, s);
+        e = launch_gemm<ProbDhPart, ProbDwHalf, kPair>(8, dev, groups, tmZk, tmWmn, tmDH, tmZmn, tmHmn, tmDW, j, eh, eb, s);
       } else {
         EpiDw::Params ew{};
         ew.accumulate = ((accumulate_dW && !rounds) || c0 > 0) ? 1 : 0;
         j.prob[1].dyn_zero_fill = ew.accumulate ? 0 : 1;
-        e = launch_gemm<ProbDh, ProbDw, kPair>(2, dev, groups, tmZk, tmWmn, tmDH, tmZmn, tmHmn, tmDW, j, eh, ew, s);
+        e = launch_gemm<ProbDhPart, ProbDw, kPair>(10, dev, groups, tmZk, tmWmn, tmDH, tmZmn, tmHmn, tmDW, j, eh, ew, s);
       }
     }
     if (e != cudaSuccess) return KD_ERR_CUDA;
-    scatter_rows_kernel<<<blocks, 256, 0, s>>>(static_cast<const uint4*>(dhc), (int)(d / 8), lp.rowmap, &live->count,
-                                               (int)c0, (int)Cc, static_cast<uint4*>(dH));
+    const int64_t finish = ceil_div(Cc * (d / 8), 256);
+    dh_finish_kernel<<<(unsigned)(finish < copy_blocks ? finish : copy_blocks), 256, 0, s>>>(
+        reinterpret_cast<const float4*>(part32), (int)(d / 8), lp.rowmap, live, (int)c0, (int)Cc, plan.k_splits,
+        static_cast<uint4*>(dH));
     if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
   }
   if (rounds) {

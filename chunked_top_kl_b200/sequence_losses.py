@@ -17,7 +17,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from .api import _grad_scalar, _on, _ptr, _raise
+from .api import _grad_scalar, _on, _ptr, _raise, _stream
 
 PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}
 KL_KINDS = {"k1": 0, "k2": 1, "k3": 2}
@@ -85,16 +85,16 @@ def _preference(logp, ref_logp, mask, offsets, beta, kind, label_smoothing, marg
     k = _choice(PREFERENCE_KINDS, kind, "kind", where)
     dev = logp.device
     grad_loss = _grad_scalar(grad_loss, dev)
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    chosen = torch.empty(lay.S // 2, dtype=torch.float32, device=dev)
-    rejected = torch.empty_like(chosen)
+    loss = logp.new_empty(())
+    chosen = logp.new_empty(lay.S // 2)
+    rejected = logp.new_empty(lay.S // 2)
     dlogp = torch.empty_like(logp) if want_grad else None
     ws = _workspace(lay.S, dev)
     with _on(dev):
         st = _abi.kd_preference_loss(_ptr(logp), _ptr(ref_logp), _ptr(mask), _ptr(offsets), lay.offsets_i64, lay.S,
                                      lay.N, float(beta), k, float(label_smoothing), float(margin),
                                      int(bool(average)), _ptr(grad_loss), _ptr(loss), _ptr(chosen), _ptr(rejected), _ptr(dlogp), _ptr(ws), ws.numel(),
-                                     torch.cuda.current_stream(dev).cuda_stream)
+                                     _stream(dev))
     _raise(st, "kd_preference_loss")
     return loss, chosen, rejected, dlogp
 
@@ -140,7 +140,7 @@ def _policy(logp, old_logp, advantages, ref_logp, mask, offsets, clip_low, clip_
     if dual_clip is not None and not dual_clip > 1.0:
         raise ValueError(f"{where}: dual_clip must be above 1, got {dual_clip}")
     grad_loss = _grad_scalar(grad_loss, dev)
-    stats = torch.empty(3, dtype=torch.float32, device=dev)
+    stats = logp.new_empty(3)
     dlogp = torch.empty_like(logp) if want_grad else None
     ws = _workspace(lay.S, dev)
     with _on(dev):
@@ -148,7 +148,7 @@ def _policy(logp, old_logp, advantages, ref_logp, mask, offsets, clip_low, clip_
                                  _ptr(mask), _ptr(offsets), lay.offsets_i64, lay.S, lay.N, float(clip_low),
                                  float(clip_high), 0.0 if dual_clip is None else float(dual_clip), float(kl_coef),
                                  k, r, _ptr(grad_loss), _ptr(stats), _ptr(dlogp), _ptr(ws), ws.numel(),
-                                 torch.cuda.current_stream(dev).cuda_stream)
+                                 _stream(dev))
     _raise(st, "kd_policy_loss")
     return (*stats.unbind(0), dlogp)
 
@@ -181,7 +181,7 @@ def _scaled(unit: torch.Tensor, grad: torch.Tensor) -> torch.Tensor:
     out = torch.empty_like(unit)
     with _on(dev):
         st = _abi.kd_scale_gradient(_ptr(unit), _ptr(g), _ptr(out), unit.numel(),
-                                    torch.cuda.current_stream(dev).cuda_stream)
+                                    _stream(dev))
     _raise(st, "kd_scale_gradient")
     return out
 

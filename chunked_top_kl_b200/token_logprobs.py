@@ -14,7 +14,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from .api import _check_buffer, _check_workspace, _on, _ptr, _raise
+from .api import _check_buffer, _check_workspace, _on, _ptr, _raise, _stream
 
 #: Tokens whose dZ rows (2 V bytes each) are held at once going back.  Larger
 #: than the distillation loss's 4096: dW is then written once, without a read
@@ -66,7 +66,7 @@ def token_logprobs_forward(H, W, labels, T: float = 1.0, entropy: bool = False,
     with _on(dev):
         st = _abi.kd_token_logp_forward(_ptr(H), _ptr(W), _ptr(labels), int(labels.dtype == torch.int64), N, d, V,
                                         float(T), _ptr(logp), _ptr(lse), _ptr(ent), _ptr(workspace), workspace.numel(),
-                                        torch.cuda.current_stream(dev).cuda_stream)
+                                        _stream(dev))
     _raise(st, "kd_token_logp_forward")
     return logp, lse, ent
 
@@ -114,7 +114,7 @@ def token_logprobs_backward(H, W, labels, lse, dlogp, T: float = 1.0, chunk: int
         st = _abi.kd_token_logp_backward(_ptr(H), _ptr(W), _ptr(labels), int(labels.dtype == torch.int64), N, d, V,
                                          float(T), int(chunk), _ptr(lse), _ptr(entropy), _ptr(dlogp), _ptr(dentropy),
                                          _ptr(dH), _ptr(dW), half, int(bool(accumulate_dW)), _ptr(workspace),
-                                         workspace.numel(), torch.cuda.current_stream(dev).cuda_stream)
+                                         workspace.numel(), _stream(dev))
     _raise(st, "kd_token_logp_backward")
     return dH, dW
 

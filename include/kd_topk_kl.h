@@ -325,8 +325,8 @@ int kd_token_logp_backward(const void* H, const void* W, const void* labels, int
  * for tokens that take no part.  grad_loss is a device fp32 scalar (the
  * upstream gradient of the loss) or NULL for 1.0.  Arrays need 4-byte
  * alignment (16-byte aligned ones are read faster), the workspace 256-byte.
- * Sums are fp64 and in a fixed order: results are deterministic.  N < 2^40,
- * S < 2^31.  The workspace's size goes by S alone. */
+ * Sums are fp64 and in a fixed order: results are deterministic.
+ * N <= 2^31 - 2^16, S < 2^31.  The workspace's size goes by S alone. */
 size_t kd_sequence_loss_workspace_size(int64_t S);
 
 /* Preference loss over S / 2 pairs (S even): sequences s and S / 2 + s are a

@@ -1,7 +1,9 @@
 // Checks the schedules of the label log-probabilities: for N tokens of which
 // any number of rows takes part, the ranges that the label scan picks keep
 // the partials inside their slots, the pacing counters inside theirs, and
-// every tile in exactly one unit.  Prints "OK <cases>" or the first failure.
+// every tile in exactly one unit; and that the dH product's cut keeps its
+// parts inside their buffer, its ranges non-empty and the pacing counters
+// inside theirs, with the scan's search picking the host's plan.  Prints "OK <cases>" or the first failure.
 #include <cstdio>
 #include <vector>
 
@@ -71,6 +73,52 @@ int main() {
           ++cases;
         }
       }
+  const long Cs[] = {1, 60, 256, 257, 1000, 4096, 8192, 12000};
+  const long ds[] = {8, 256, 264, 1000, 2048, 2880, 8192};
+  for (long C : Cs)
+    for (long V : Vs)
+      for (long d : ds)
+        for (int G : groups)
+          for (int with_dW = 0; with_dW < 2; ++with_dW)
+            for (long k = 1; k <= 12; ++k) {
+              const long rows = k <= 10 ? (k * C + 9) / 10 : (k == 11 ? 1 : C / 2 + 1);
+              const int64_t bands = ceil_div64(rows, 256), cols = ceil_div64(d, 256), k0 = ceil_div64(V, 64);
+              const int64_t U1 = with_dW ? ceil_div64(V, 256) * cols : 0, k1 = with_dW ? ceil_div64(rows, 64) : 0;
+              const int64_t room = dh_part_rows(C);
+              const DhPlan p = dh_plan(bands, cols, d, k0, U1, k1, G, room);
+              unsigned long long best = ~0ull;
+              for (int i = 0; i < 2 * kMaxDhSplits; ++i) {
+                bool wide;
+                int ks;
+                dh_candidate(i, wide, ks);
+                const int64_t c = dh_cost(bands, cols, d, k0, U1, k1, G, wide, ks, room);
+                if (c >= 0) {
+                  if (c >= (int64_t(1) << 32)) { printf("FAIL cost %ld\n", (long)c); return 1; }
+                  const unsigned long long key = ((unsigned long long)c << 32) | (unsigned)i;
+                  if (key < best) best = key;
+                }
+              }
+              const DhPlan q = dh_plan_of((int)(unsigned)best, cols);
+              if (p.k_splits != q.k_splits || p.k_cols != q.k_cols || p.wide_cols != q.wide_cols) {
+                printf("FAIL the scan's cut differs: C %ld V %ld d %ld rows %ld\n", C, V, d, rows);
+                return 1;
+              }
+              if (p.k_splits < 1 || p.k_splits > k0 || bands * 256 * p.k_splits > room ||
+                  p.k_cols != (p.wide_cols ? ceil_div64(cols, 2) : cols) || (p.wide_cols && p.wide_cols != cols)) {
+                printf("FAIL cut %d of %ld K blocks, %ld bands in %ld rows\n", p.k_splits, (long)k0, (long)bands, (long)room);
+                return 1;
+              }
+              const int64_t counters = wave_slots_bound(room / 256 * cols, ceil_div64(V, 256) * cols);
+              if (wave_slots_bound(bands * p.k_cols * p.k_splits, U1) > counters) { printf("FAIL counters\n"); return 1; }
+              int64_t at = 0;                 // the K ranges follow one another, none empty
+              for (int part = 0; part < p.k_splits; ++part) {
+                const int64_t a = k0 * part / p.k_splits, b = k0 * (part + 1) / p.k_splits;
+                if (a != at || b <= a) { printf("FAIL range %d of %d\n", part, p.k_splits); return 1; }
+                at = b;
+              }
+              if (at != k0) { printf("FAIL ranges end at %ld\n", (long)at); return 1; }
+              ++cases;
+            }
   printf("OK %ld\n", cases);
   return 0;
 }
