@@ -303,7 +303,49 @@ struct EpiLogp {
   }
 };
 
-// Joins the column ranges' partials of 32 rows per block, 8 threads a row.
+// A row's state over some of the columns: m (the scaled maximum mb of
+// EpiLogp), s, t and the label's logit, 0 where the columns do not hold it.
+template <bool ENT>
+struct LogpState {
+  float m, s, t, g;
+
+  __device__ __forceinline__ void clear() {
+    m = -INFINITY;
+    s = t = g = 0.f;
+  }
+  __device__ __forceinline__ void join(const LogpState& o) {
+    const float top = fmaxf(m, o.m);
+    const float d1 = m == top ? 0.f : m - top, d2 = o.m == top ? 0.f : o.m - top;
+    const float f1 = ex2_approx(d1), f2 = ex2_approx(d2);
+    if (ENT) t = (f1 > 0.f ? f1 * fmaf(d1, s, t) : 0.f) + (f2 > 0.f ? f2 * fmaf(d2, o.s, o.t) : 0.f);
+    s = fmaf(f1, s, f2 * o.s);
+    g += o.g;
+    m = top;
+  }
+  // One more column's logit.
+  __device__ __forceinline__ void add(float z, float zl2) {
+    const float mb = fmaxf(m, z * zl2);
+    if (mb > m) {
+      const float delta = m - mb, f = ex2_approx(delta);
+      if (ENT) t = f > 0.f ? f * fmaf(delta, s, t) : 0.f;
+      s *= f;
+      m = mb;
+    }
+    const float u = fmaf(z, zl2, -m), e = ex2_approx(u);
+    s += e;
+    if (ENT) t = fmaf(e, u, t);
+  }
+  __device__ __forceinline__ LogpState shuffled(int o) const {
+    LogpState r;
+    r.m = __shfl_xor_sync(0xffffffffu, m, o);
+    r.s = __shfl_xor_sync(0xffffffffu, s, o);
+    r.t = ENT ? __shfl_xor_sync(0xffffffffu, t, o) : 0.f;
+    r.g = __shfl_xor_sync(0xffffffffu, g, o);
+    return r;
+  }
+};
+
+// Joins the column ranges' partials of a row.
 // The label's term is then exchanged for that of its exact logit z_y (see
 // gather_live_kernel; the products' own g serves to take the old term out):
 // with u = g zl2 - M, u' = z_y log2(e) / T - M,
@@ -313,53 +355,257 @@ struct EpiLogp {
 //   ent = ln 2 (log2 s - t / s):
 // the label's logit meets M before the logarithm is added, so that a
 // confident token's small log-probability is not the rest of two large terms.
-constexpr int kLogpMergeRows = 32, kLogpMergeLanes = 8;
-
-template <bool ENT>
-__global__ void __launch_bounds__(kLogpMergeRows * kLogpMergeLanes)
+//
+// ROWS rows a block, LANES threads a row: 32 and 8 for the GEMM's few ranges,
+// one row and 256 threads for the many of logp_few_kernel.
+template <bool ENT, int ROWS, int LANES>
+__global__ void __launch_bounds__(ROWS * LANES)
 logp_merge_kernel(const float* __restrict__ part_m, const float* __restrict__ part_s, const float* __restrict__ part_t,
                   const float* __restrict__ part_g, const LiveRows* __restrict__ live,
                   const int32_t* __restrict__ rowmap, const float* __restrict__ zlab, float zl2, float zl2_exact,
-                  float* __restrict__ logp, float* __restrict__ lse,
-                  float* __restrict__ ent, const Status* __restrict__ status) {
-  __shared__ float s_m[kLogpMergeLanes][kLogpMergeRows], s_s[kLogpMergeLanes][kLogpMergeRows],
-      s_t[kLogpMergeLanes][kLogpMergeRows], s_g[kLogpMergeLanes][kLogpMergeRows];
+                  float* __restrict__ logp, float* __restrict__ lse, float* __restrict__ ent,
+                  const Status* __restrict__ status) {
+  __shared__ LogpState<ENT> s_part[LANES][ROWS];
   const int rows = live->count, splits = live->raster.splits;
-  const int x = threadIdx.x & (kLogpMergeRows - 1), y = threadIdx.x / kLogpMergeRows;
-  const int q = blockIdx.x * kLogpMergeRows + x;
-  float m = -INFINITY, s = 0.f, t = 0.f, g = 0.f;
-  auto join = [&](float m2, float s2, float t2, float g2) {
-    const float top = fmaxf(m, m2);
-    const float d1 = m == top ? 0.f : m - top, d2 = m2 == top ? 0.f : m2 - top;
-    const float f1 = ex2_approx(d1), f2 = ex2_approx(d2);
-    if (ENT) t = (f1 > 0.f ? f1 * fmaf(d1, s, t) : 0.f) + (f2 > 0.f ? f2 * fmaf(d2, s2, t2) : 0.f);
-    s = fmaf(f1, s, f2 * s2);
-    g += g2;                                // the label's range holds it, the others 0
-    m = top;
-  };
+  const int x = threadIdx.x % ROWS, y = threadIdx.x / ROWS;
+  const int q = blockIdx.x * ROWS + x;
+  LogpState<ENT> st;
+  st.clear();
   if (q < rows)
-    for (int k = y; k < splits; k += kLogpMergeLanes) {
+    for (int k = y; k < splits; k += LANES) {
       const size_t o = (size_t)k * rows + q;
-      join(part_m[o], part_s[o], ENT ? part_t[o] : 0.f, part_g[o]);
+      LogpState<ENT> other;
+      other.m = part_m[o];
+      other.s = part_s[o];
+      other.t = ENT ? part_t[o] : 0.f;
+      other.g = part_g[o];
+      st.join(other);
     }
-  s_m[y][x] = m;
-  s_s[y][x] = s;
-  s_t[y][x] = t;
-  s_g[y][x] = g;
-  __syncthreads();
+  s_part[y][x] = st;
+#pragma unroll
+  for (int w = LANES / 2; w > 0; w >>= 1) {
+    __syncthreads();
+    if (y < w) {
+      st.join(s_part[y + w][x]);
+      s_part[y][x] = st;
+    }
+  }
   if (y == 0 && q < rows) {
-    for (int k = 1; k < kLogpMergeLanes && k < splits; ++k) join(s_m[k][x], s_s[k][x], s_t[k][x], s_g[k][x]);
     const int n = rowmap[q];
-    const float ug = fmaf(g, zl2, -m), uy = fmaf(zlab[q], zl2_exact, -m);
+    const float ug = fmaf(st.g, zl2, -st.m), uy = fmaf(zlab[q], zl2_exact, -st.m);
     const float eg = exp2f(ug), more = eg * expm1f((uy - ug) * kLn2);
-    s += more;
-    if (ENT) t += fmaf(more, uy, eg * (uy - ug));
-    const float l2 = log2f(s);
+    st.s += more;
+    const float l2 = log2f(st.s);
     const bool failed = *reinterpret_cast<const volatile unsigned int*>(&status->timeout) != 0u;
     const float nan = __int_as_float(0x7fc00000);
     logp[n] = failed ? nan : kLn2 * (uy - l2);
-    lse[n] = failed ? nan : kLn2 * (m + l2);
-    if (ENT) ent[n] = failed ? nan : kLn2 * (l2 - t / s);
+    lse[n] = failed ? nan : kLn2 * (st.m + l2);
+    if (ENT) {
+      st.t += fmaf(more, uy, eg * (uy - ug));
+      ent[n] = failed ? nan : kLn2 * (l2 - st.t / st.s);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- a few tokens
+//
+// Up to kFewTokens tokens (a single token's score, a draft to verify): the
+// time is that of reading W once, 2 V d bytes, and the GEMM above, whose tiles
+// are 256 tokens high, reads it at 4.6 TB/s (250 us at V = 201,088, d = 2880,
+// one token).  Here each warp streams a contiguous range of W's rows straight
+// into registers, sixteen rows at a time, as the A operand of m16n8k16 products
+// with the tokens as columns: the tensor cores idle nearly all of the time, so
+// the plain warp-level product serves.  A thread's 16-byte load holds eight
+// consecutive k of a row where the product's layout wants two groups of two
+// times two; as every k counts alike, A and B take the same eight in the same
+// order.  H lies in shared memory in the order of the loads (few_smem bytes: a
+// d that does not fit goes to the GEMM); read through L1 it was pushed out by
+// the stream of W (206 us instead of 195 us for a token, 316 instead of 223 for nine).  The
+// running softmax state is as in EpiLogp, a thread holding two tokens (per eight) over the rows it meets;
+// warps, then blocks (through the partials, one range per block) are joined.
+//
+// Every kFewBatch k blocks the products start from zero and are added up in
+// fp32 with rounding: sums so short need no accumulation_gain.
+constexpr int kFewTokens = 16;
+constexpr int kFewWarps = 8, kFewThreads = 32 * kFewWarps;
+constexpr int kFewBatch = 4;                  // k blocks of 32 whose loads are in flight together
+constexpr int kFewBlocksPerSm = 2;            // one wave: the ranges are even
+
+// Bytes of H in shared memory for N tokens, and the most that two blocks of an SM can have.
+KD_HD int64_t few_smem(int64_t N, int64_t d) { return ceil_div64(N, 8) * ceil_div64(d, 32) * 512; }
+constexpr int64_t kFewSmem = 110 * 1024;
+
+struct FewArgs {
+  const uint4 *H, *W;
+  const void* labels;
+  int labels_i64, N, V, d8;
+  float zl2;
+  float *logp, *lse, *ent;
+  int32_t* rowmap;
+  LiveRows* live;
+  Status* status;
+  float *zlab, *part_m, *part_s, *part_t, *part_g;
+};
+
+__device__ __forceinline__ void mma_m16n8k16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int NT, bool ENT>
+__global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) logp_few_kernel(const FewArgs A) {
+  __shared__ int s_tok[kFewTokens], s_lab[kFewTokens];
+  __shared__ LogpState<ENT> s_part[kFewWarps][8 * NT];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  // every warp finds the live tokens; block 0 says so to the merge
+  int64_t y = -1;
+  if (lane < A.N)
+    y = A.labels_i64 ? static_cast<const int64_t*>(A.labels)[lane] : (int64_t) static_cast<const int32_t*>(A.labels)[lane];
+  const bool on = y >= 0 && y < A.V;
+  const unsigned live = __ballot_sync(0xffffffffu, on), wrong = __ballot_sync(0xffffffffu, y >= A.V);
+  const int rows = __popc(live), q = __popc(live & ((1u << lane) - 1u));
+  if (warp == 0) {
+    if (on) {
+      s_tok[q] = lane;
+      s_lab[q] = (int)y;
+    }
+    if (blockIdx.x == 0) {
+      if (on) A.rowmap[q] = lane;
+      if (lane < A.N && !on) {
+        const float v = y >= A.V ? __int_as_float(0x7fc00000) : 0.f;
+        A.logp[lane] = v;
+        A.lse[lane] = v;
+        if (ENT) A.ent[lane] = v;
+      }
+      if (lane == 0) {
+        A.live->count = rows;
+        A.live->raster.splits = (int)gridDim.x;
+        A.status->bad_index = __popc(wrong);
+        A.status->timeout = 0u;
+      }
+    }
+  }
+  __syncthreads();
+  if (rows == 0) return;
+  // the exact label logits, a row per block (see gather_live_kernel)
+  if (warp == 0)
+    for (int r = blockIdx.x; r < rows; r += gridDim.x) {
+      const uint4 *h = A.H + (size_t)s_tok[r] * A.d8, *w = A.W + (size_t)s_lab[r] * A.d8;
+      double z = 0.0;
+      for (int j = lane; j < A.d8; j += 32) z += (double)dot8(h[j], w[j]);
+      z = warp_sum_d(z);
+      if (lane == 0) A.zlab[r] = (float)z;
+    }
+  // H: for each eight tokens and k block of 32, lane (g, t)'s eight k of token g
+  extern __shared__ uint4 s_h[];
+  const int kblocks = (A.d8 + 3) / 4;
+  for (int i = threadIdx.x; i < NT * kblocks * 32; i += kFewThreads) {
+    const int nt = i / (kblocks * 32), k = (i / 32 % kblocks) * 4 + (i & 3), n = 8 * nt + ((i & 31) >> 2);
+    s_h[i] = n < rows && k < A.d8 ? A.H[(size_t)s_tok[n] * A.d8 + k] : make_uint4(0u, 0u, 0u, 0u);
+  }
+  __syncthreads();
+  int lab[2 * NT];                            // labels of the tokens whose logits it gets: 2 t and 2 t + 1
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) lab[2 * nt + j] = 8 * nt + 2 * t + j < rows ? s_lab[8 * nt + 2 * t + j] : -1;
+  }
+  LogpState<ENT> st[2 * NT];
+#pragma unroll
+  for (int i = 0; i < 2 * NT; ++i) st[i].clear();
+
+  const int64_t w = (int64_t)blockIdx.x * kFewWarps + warp, nw = (int64_t)gridDim.x * kFewWarps;
+  const int r0 = (int)(A.V * w / nw), r1 = (int)(A.V * (w + 1) / nw);
+  float z[NT][4];
+  // the batch of row r, k blocks from k0; rows past the range repeat its last one, and do not count
+  auto load = [&](int r, int k0, uint4 (&va)[kFewBatch], uint4 (&vb)[kFewBatch]) {
+    const uint4* pa = A.W + (size_t)(r + g < r1 ? r + g : r1 - 1) * A.d8;
+    const uint4* pb = A.W + (size_t)(r + g + 8 < r1 ? r + g + 8 : r1 - 1) * A.d8;
+#pragma unroll
+    for (int u = 0; u < kFewBatch; ++u) {
+      const int k = k0 + 4 * u + t;
+      va[u] = vb[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (k < A.d8) {
+        va[u] = __ldcs(pa + k);
+        vb[u] = __ldcs(pb + k);
+      }
+    }
+  };
+  auto multiply = [&](int r, int k0, const uint4 (&va)[kFewBatch], const uint4 (&vb)[kFewBatch]) {
+    if (k0 == 0) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[nt][j] = 0.f;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int u = 0; u < kFewBatch; ++u) {
+        const int kb = k0 / 4 + u;              // W is zero past d, H there is not read past its last block
+        const uint4 h = s_h[(nt * kblocks + (kb < kblocks ? kb : kblocks - 1)) * 32 + lane];
+        mma_m16n8k16(c, va[u].x, vb[u].x, va[u].y, vb[u].y, h.x, h.y);
+        mma_m16n8k16(c, va[u].z, vb[u].z, va[u].w, vb[u].w, h.z, h.w);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[nt][j] += c[j];
+    }
+    if (k0 + 4 * kFewBatch < A.d8) return;
+    const int ra = r + g, rb = r + g + 8;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        LogpState<ENT>& x = st[2 * nt + j];
+        if (ra < r1) x.add(z[nt][j], A.zl2);
+        if (rb < r1) x.add(z[nt][j + 2], A.zl2);
+        if (lab[2 * nt + j] == ra && ra < r1) x.g = z[nt][j];
+        if (lab[2 * nt + j] == rb && rb < r1) x.g = z[nt][j + 2];
+      }
+  };
+  auto step = [&](int& r, int& k0) {          // to the next batch
+    k0 += 4 * kFewBatch;
+    if (k0 >= A.d8) {
+      k0 = 0;
+      r += 16;
+    }
+  };
+  // two batches in registers: one is multiplied while the other arrives
+  uint4 va[kFewBatch], vb[kFewBatch], wa[kFewBatch], wb[kFewBatch];
+  int r = r0, k0 = 0;
+  if (r < r1) load(r, k0, va, vb);
+  while (r < r1) {
+    int r2 = r, k2 = k0;
+    step(r2, k2);
+    if (r2 < r1) load(r2, k2, wa, wb);
+    multiply(r, k0, va, vb);
+    if (r2 >= r1) break;
+    r = r2;
+    k0 = k2;
+    step(r, k0);
+    if (r < r1) load(r, k0, va, vb);
+    multiply(r2, k2, wa, wb);
+  }
+#pragma unroll
+  for (int i = 0; i < 2 * NT; ++i) {          // over the eight lanes with the same tokens
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) st[i].join(st[i].shuffled(o));
+    if (g == 0) s_part[warp][8 * (i / 2) + 2 * t + (i & 1)] = st[i];
+  }
+  __syncthreads();
+  const int n = threadIdx.x;
+  if (n < rows) {
+    LogpState<ENT> x = s_part[0][n];
+    for (int k = 1; k < kFewWarps; ++k) x.join(s_part[k][n]);
+    const size_t o = (size_t)blockIdx.x * rows + n;
+    A.part_m[o] = x.m;
+    A.part_s[o] = x.s;
+    A.part_g[o] = x.g;
+    if (ENT) A.part_t[o] = x.t;
   }
 }
 

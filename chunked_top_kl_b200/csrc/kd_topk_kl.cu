@@ -8,7 +8,8 @@
 //                      gemm<EpiDz> -> gemm<EpiDh + EpiDw> [-> scatter_rows]
 //                      (bracketed steps: skipping masked rows)
 // Label log-probabilities: label_prep -> gather_live -> gemm<EpiLogp> ->
-//                      logp_merge; gradient: label_prep -> for each chunk,
+//                      logp_merge, or logp_few -> logp_merge for a few tokens;
+//                      gradient: label_prep -> for each chunk,
 //                      gather_live -> gemm<EpiDlogp> -> gemm<EpiDhPart + EpiDw
 //                      or EpiDwHalf> -> dh_finish
 // Teacher top-K cache writer: for each chunk, gemm<EpiZ32> (fp32 logits and
@@ -954,8 +955,53 @@ int logp_forward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, 
   if (launch_one<ProbLogp<ENT>>(ENT ? 5 : 4, dev, lp.groups, tmH, tmW, tmH, a, lp.status, ep, s,
                                 DynRows{&live->count, 0, (int)N, &live->raster}, wave) != cudaSuccess)
     return KD_ERR_CUDA;
-  logp_merge_kernel<ENT><<<(unsigned)ceil_div(N, kLogpMergeRows), kLogpMergeRows * kLogpMergeLanes, 0, s>>>(
+  logp_merge_kernel<ENT, 32, 8><<<(unsigned)ceil_div(N, 32), 256, 0, s>>>(
       ep.part_m, ep.part_s, ep.part_t, ep.part_g, live, lp.rowmap, zlab, ep.zl2, kLog2e / T, logp, lse, ent, lp.status);
+  return cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;
+}
+
+template <bool ENT>
+int logp_forward_few(const void* H, const void* W, const void* labels, int labels_i64, int64_t N, int64_t d, int64_t V,
+                     float T, float* logp, float* lse, float* ent, const LogpLayout& L, void* ws, int dev,
+                     cudaStream_t s) {
+  FewArgs a{};
+  a.H = static_cast<const uint4*>(H);
+  a.W = static_cast<const uint4*>(W);
+  a.labels = labels;
+  a.labels_i64 = labels_i64;
+  a.N = (int)N;
+  a.V = (int)V;
+  a.d8 = (int)(d / 8);
+  a.zl2 = kLog2e / T;
+  a.logp = logp;
+  a.lse = lse;
+  a.ent = ent;
+  a.rowmap = at<int32_t>(ws, L.off_rowmap);
+  a.live = at<LiveRows>(ws, L.off_live);
+  a.status = at<Status>(ws, L.off_status);
+  a.zlab = at<float>(ws, L.off_zlab);
+  float* part = at<float>(ws, L.off_part);
+  a.part_m = part;
+  a.part_s = part + L.slots;
+  a.part_g = part + 2 * L.slots;
+  a.part_t = part + 3 * L.slots;
+  // a range of at least 16 rows for each warp, and a partial slot for each block and token
+  int64_t blocks = (int64_t)device_sms(dev) * kFewBlocksPerSm, want = ceil_div(V, 16 * kFewWarps);
+  if (blocks > want) blocks = want;
+  if (blocks > L.slots / N) blocks = L.slots / N;
+  const unsigned grid = (unsigned)blocks;
+  auto kern = N <= 8 ? logp_few_kernel<1, ENT> : logp_few_kernel<2, ENT>;
+  const int slot = (N <= 8 ? 11 : 12) + (ENT ? 2 : 0);
+  if (dev < 0 || dev >= kMaxDevices) return KD_ERR_UNSUPPORTED;
+  if (!g_dev[dev].attr_set[slot]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmem) != cudaSuccess)
+      return KD_ERR_CUDA;
+    g_dev[dev].attr_set[slot] = true;
+  }
+  kern<<<grid, kFewThreads, (size_t)few_smem(N, d), s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
+  logp_merge_kernel<ENT, 1, 256><<<(unsigned)N, 256, 0, s>>>(a.part_m, a.part_s, a.part_t, a.part_g, a.live, a.rowmap,
+                                                            a.zlab, a.zl2, a.zl2, logp, lse, ent, a.status);
   return cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;
 }
 
@@ -1124,6 +1170,9 @@ int kd_token_logp_forward(const void* H, const void* W, const void* labels, int 
                                                                                                      : KD_ERR_CUDA;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KD_ERR_CUDA;
+  if (N <= kFewTokens && few_smem(N, d) <= kFewSmem)
+    return entropy ? logp_forward_few<true>(H, W, labels, labels_i64, N, d, V, T, logp, lse, entropy, L, workspace, dev, s)
+                   : logp_forward_few<false>(H, W, labels, labels_i64, N, d, V, T, logp, lse, nullptr, L, workspace, dev, s);
   const LabelPrep lp = label_prep(labels, labels_i64, N, V, L, workspace);
   return entropy ? logp_forward<true>(H, W, N, d, V, T, logp, lse, entropy, L, workspace, dev, s, lp)
                  : logp_forward<false>(H, W, N, d, V, T, logp, lse, nullptr, L, workspace, dev, s, lp);

@@ -130,6 +130,20 @@ def test_both_passes(kd, N, d, V, ignored, i64, T, ent):
     _check_backward(dH4, None, H, W, y, g, h if ent else None, T)
 
 
+@pytest.mark.parametrize("N", [1, 7, 8, 9, 16, 17, 31, 32, 33])
+@pytest.mark.parametrize("d,V", [(8, 3), (40, 129), (1000, 5003), (2880, 40000)])
+@pytest.mark.parametrize("ignored", ["none", "some"])
+def test_a_few_tokens(kd, N, d, V, ignored):
+    """Both sides of the border between the streaming pass and the GEMM, with and without entropies, and a token
+    that the labels leave out in any place."""
+    H, W, y, _, _ = _inputs(N, d, V, N + d, ignored)
+    if ignored == "some":
+        y[0] = -1
+    for ent in (False, True):
+        out = kd.token_logprobs_forward(H.cuda(), W.cuda(), y.cuda(), 0.9, entropy=ent)
+        _check_forward(out, H, W, y, 0.9)
+
+
 def test_confident_tokens(kd):
     """Labels at probabilities from 1e-3 to 1 - 1e-6: log-probabilities near 0 and p - 1 keep their precision."""
     H, W, y, g, _ = _inputs(300, 64, 500, 3, "none", pull=60.0)
