@@ -89,13 +89,31 @@ int run_preference(const PrefArgs& A, cudaStream_t s) {
   return launched();
 }
 
-template <int TEAM, bool VEC>
+template <int TEAM, bool VEC, int KL>
 int run_policy(PolicyArgs A, cudaStream_t s) {
+  const int blocks = (int)blocks_for(A.q, TEAM, kLossBlocks);
+  if (A.per_sequence && A.q.splits == 1) {
+    A.sums = nullptr;
+    policy_loss_kernel<TEAM, VEC, KL><<<blocks, kThreads, 0, s>>>(A);
+    if (launched() != KD_OK) return KD_ERR_CUDA;
+    policy_finish_kernel<<<1, kThreads, 0, s>>>(A, blocks);
+    return launched();
+  }
   A.sum_blocks = (int)blocks_for(A.q, TEAM, kSumBlocks);
   policy_sums_kernel<TEAM, VEC><<<A.sum_blocks, kThreads, 0, s>>>(A);
   if (launched() != KD_OK) return KD_ERR_CUDA;
-  policy_loss_kernel<TEAM, VEC><<<blocks_for(A.q, TEAM, kLossBlocks), kThreads, 0, s>>>(A);
+  policy_loss_kernel<TEAM, VEC, KL><<<blocks, kThreads, 0, s>>>(A);
   return launched();
+}
+
+template <int TEAM, bool VEC>
+int run_policy_kl(int kl, const PolicyArgs& A, cudaStream_t s) {
+  switch (kl) {
+    case kK1: return run_policy<TEAM, VEC, kK1>(A, s);
+    case kK2: return run_policy<TEAM, VEC, kK2>(A, s);
+    case kK3: return run_policy<TEAM, VEC, kK3>(A, s);
+    default: return run_policy<TEAM, VEC, kNoKl>(A, s);
+  }
 }
 
 }  // namespace
@@ -180,13 +198,15 @@ int kd_policy_loss(const float* logp, const float* old_logp, const float* ref_lo
   A.grad_loss = grad_loss;
   A.adv_per_seq = advantages_per_sequence;
   A.per_sequence = per_sequence;
-  A.kl_kind = kl_kind;
-  A.dual = dual_clip != 0.0;
   two_floats(std::log1p(clip_high), &A.hi_h, &A.hi_l);
   two_floats(std::log1p(-clip_low), &A.lo_h, &A.lo_l);
-  two_floats(A.dual ? std::log(dual_clip) : 0.0, &A.dual_h, &A.dual_l);
-  A.hi = (float)clip_high;
-  A.lo = (float)clip_low;
+  two_floats(std::log(dual_clip), &A.dual_h, &A.dual_l);
+  if (dual_clip == 0.0) {
+    A.dual_h = INFINITY;
+    A.dual_l = 0.f;
+  }
+  A.hi1 = (float)(1.0 + clip_high);
+  A.lo1 = (float)(1.0 - clip_low);
   A.dual_c = (float)dual_clip;
   A.kl_coef = (float)kl_coef;
   A.sums = reinterpret_cast<double*>(ws + L.off_sums);
@@ -197,8 +217,9 @@ int kd_policy_loss(const float* logp, const float* old_logp, const float* ref_lo
   A.dlogp = dlogp;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool vec = all_aligned16({logp, old_logp, ref_logp, advantages_per_sequence ? nullptr : advantages, mask, dlogp});
-  if (team == 32) return vec ? run_policy<32, true>(A, s) : run_policy<32, false>(A, s);
-  return vec ? run_policy<kThreads, true>(A, s) : run_policy<kThreads, false>(A, s);
+  const int kl = ref_logp ? kl_kind : kNoKl;
+  if (team == 32) return vec ? run_policy_kl<32, true>(kl, A, s) : run_policy_kl<32, false>(kl, A, s);
+  return vec ? run_policy_kl<kThreads, true>(kl, A, s) : run_policy_kl<kThreads, false>(kl, A, s);
 }
 
 int kd_scale_gradient(const float* x, const float* g, float* out, int64_t N, void* stream) {

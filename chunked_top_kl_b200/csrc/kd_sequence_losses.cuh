@@ -7,7 +7,10 @@
 // launches: the first sums what the second has to divide by or compare with
 // (a sequence's log ratio, the mask), the second reads the tokens, writes the
 // gradient and reduces the scalars.  The gradient thus comes with the loss,
-// in one reading of everything but the mask.
+// in one reading of everything but the mask.  A policy loss that is averaged
+// per sequence, with a team for each sequence, needs no such first launch: the
+// team sums its sequence's mask and finds it in L1 when it reads it again; a
+// one-block launch then joins the scalars.
 //
 // Work is cut into items: a sequence, or one of `splits` ranges of it when the
 // sequences are few and long.  A team (a warp for short sequences, a block
@@ -243,6 +246,13 @@ __global__ void __launch_bounds__(kThreads, 4) pref_loss_kernel(const PrefArgs A
   for (int64_t it = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; it < items; it += (int64_t)gridDim.x * kTeams) {
     const int64_t s = it / A.q.splits;
     const int k = (int)(it - s * A.q.splits);
+    int lo, hi;
+    item_range(A.q, s, k, lo, hi);
+    float m[kSumUnroll][4];                   // the first groups' masks arrive while the coefficient is worked out
+    if (A.dlogp)
+#pragma unroll
+      for (int u = 0; u < kSumUnroll; ++u)
+        load_mask4<VEC>(A.mask, (((lo >> 2) + tid) << 2) + 4 * TEAM * u, lo, hi, m[u]);
     float coef = 0.f;
     if (tid < 32) {
       const bool is_chosen = s < P;
@@ -280,19 +290,19 @@ __global__ void __launch_bounds__(kThreads, 4) pref_loss_kernel(const PrefArgs A
       coef = s_coef;
       __syncthreads();
     }
-    int lo, hi;
-    item_range(A.q, s, k, lo, hi);
     for (int t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM * kSumUnroll) {
-      float m[kSumUnroll][4];
+      float d[kSumUnroll][4];
 #pragma unroll
-      for (int u = 0; u < kSumUnroll; ++u) load_mask4<VEC>(A.mask, t0 + 4 * TEAM * u, lo, hi, m[u]);
+      for (int u = 0; u < kSumUnroll; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[u][j] = m[u][j] != 0.f ? coef * m[u][j] : 0.f;
+#pragma unroll
+      for (int u = 0; u < kSumUnroll; ++u)
+        load_mask4<VEC>(A.mask, t0 + 4 * TEAM * (u + kSumUnroll), lo, hi, m[u]);
 #pragma unroll
       for (int u = 0; u < kSumUnroll; ++u) {
         const int t = t0 + 4 * TEAM * u;
-        float d[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) d[j] = m[u][j] != 0.f ? coef * m[u][j] : 0.f;
-        if (t < hi) store4<VEC>(A.dlogp, t, lo, hi, d);
+        if (t < hi) store4<VEC>(A.dlogp, t, lo, hi, d[u]);
       }
     }
   }
@@ -321,28 +331,42 @@ __global__ void __launch_bounds__(kThreads, 4) pref_loss_kernel(const PrefArgs A
 // treats old, ref and A as constants.
 //
 // Whether a token is clipped is decided on the exact difference x, against
-// log(1 + hi), log(1 - lo) and log c: x as a float and the float it was rounded
-// by, the border as a float and the rest of it (see above_border).  So the
-// decision is the formula's and not that of a rounded exponential.  e^x and
-// the KL term are taken in 32 bits; e^-y - 1 + y, which cancels for small y,
-// by its series for |y| < 1/2.  Tokens are computed without branches, masked
-// ones on zeros: four at a time in flight instead of one behind the other.
+// log(1 + hi), log(1 - lo) and log c, and not on a rounded exponential.  e^x and
+// the KL term are taken in 32 bits (ex2.approx: 2^-22); e^-y - 1 + y, which
+// cancels for small y, by its series for |y| < 1/2.  Tokens are computed
+// without branches, masked ones on zeros: four at a time in flight instead of
+// one behind the other.
 
-enum { kK1 = 0, kK2 = 1, kK3 = 2 };
+enum { kK1 = 0, kK2 = 1, kK3 = 2, kNoKl = 3 };
 
 struct PolicyArgs {
   Sequences q;
   const float *logp, *old, *ref, *adv, *mask, *grad_loss;
-  int adv_per_seq, per_sequence, kl_kind, dual;
-  float hi_h, hi_l, lo_h, lo_l, dual_h, dual_l;     // log borders, in two floats each
-  float hi, lo, dual_c, kl_coef;
-  double* sums;            // [S * splits] sum m
+  int adv_per_seq, per_sequence;
+  float hi_h, hi_l, lo_h, lo_l, dual_h, dual_l;     // log borders in two floats each (no dual clip: infinity)
+  float hi1, lo1, dual_c, kl_coef;                  // 1 + hi, 1 - lo, c
+  double* sums;            // [S * splits] sum m; null: each team sums its own (whole) sequences' masks
   double* total;           // [kSumBlocks] the first launch's blocks' sums
   int sum_blocks;
   double* part;            // [blocks][3]
   unsigned int* counter;
   float *loss, *dlogp;     // loss[3]: loss, KL, clipped share
 };
+
+// A thread's share of the sum of the mask over [lo, hi).
+template <int TEAM, bool VEC>
+__device__ __forceinline__ double mask_sum(const float* __restrict__ mask, int lo, int hi, int tid) {
+  double n = 0.0;
+  for (int t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM * kSumUnroll) {
+    float m[kSumUnroll][4];
+#pragma unroll
+    for (int u = 0; u < kSumUnroll; ++u) load4<VEC>(mask, t0 + 4 * TEAM * u, lo, hi, m[u]);
+#pragma unroll
+    for (int u = 0; u < kSumUnroll; ++u)
+      n += ((double)m[u][0] + (double)m[u][1]) + ((double)m[u][2] + (double)m[u][3]);
+  }
+  return n;
+}
 
 template <int TEAM, bool VEC>
 __global__ void __launch_bounds__(kThreads, 8) policy_sums_kernel(const PolicyArgs A) {
@@ -356,20 +380,7 @@ __global__ void __launch_bounds__(kThreads, 8) policy_sums_kernel(const PolicyAr
     const int64_t s = it / A.q.splits;
     int lo, hi;
     item_range(A.q, s, (int)(it - s * A.q.splits), lo, hi);
-    double n = 0.0;
-    if (A.mask) {
-      for (int t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM * kSumUnroll) {
-        float m[kSumUnroll][4];
-#pragma unroll
-        for (int u = 0; u < kSumUnroll; ++u) load4<VEC>(A.mask, t0 + 4 * TEAM * u, lo, hi, m[u]);
-#pragma unroll
-        for (int u = 0; u < kSumUnroll; ++u)
-          n += ((double)m[u][0] + (double)m[u][1]) + ((double)m[u][2] + (double)m[u][3]);
-      }
-      n = team_sum<TEAM>(n, red);
-    } else {
-      n = (double)(hi - lo);
-    }
+    const double n = A.mask ? team_sum<TEAM>(mask_sum<TEAM, VEC>(A.mask, lo, hi, tid), red) : (double)(hi - lo);
     if (tid == 0) {
       A.sums[it] = n;
       all += n;
@@ -377,6 +388,12 @@ __global__ void __launch_bounds__(kThreads, 8) policy_sums_kernel(const PolicyAr
   }
   all = team_sum<kThreads>(all, red);
   if (threadIdx.x == 0) A.total[blockIdx.x] = all;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // (e^x - 1 - x) / x^2 for |x| < 1/2: sum_k x^k / (k + 2)!, k = 0..8 (the next term is below 2^-31 of it).
@@ -392,36 +409,43 @@ __device__ __forceinline__ float exp_tail_series(float x) {
   return fmaf(p, x, 0.5f);
 }
 
-// Sign of (x + rest) - (h + l): x - h is exact near the border, and far from it the rests decide nothing.
-__device__ __forceinline__ float above_border(float x, float rest, float h, float l) {
-  return __fadd_rn(__fsub_rn(x, h), __fsub_rn(rest, l));
+// What the rounding of x = lp - old left out, exactly.
+__device__ __forceinline__ float difference_rest(float lp, float old, float x) {
+  const float b = __fsub_rn(x, lp);
+  return __fsub_rn(__fsub_rn(lp, __fsub_rn(x, b)), __fadd_rn(old, b));
 }
 
 // One token: its loss, KL estimate, whether it is clipped, and d loss / d logp.
+template <int KL>
 __device__ __forceinline__ void policy_token(const PolicyArgs& A, float lp, float old, float ref, float a, float& loss,
                                              float& kl, float& clipped, float& d) {
-  const float x = __fsub_rn(lp, old), b = __fsub_rn(x, lp);
-  float rest = __fsub_rn(__fsub_rn(lp, __fsub_rn(x, b)), __fadd_rn(old, b));    // lp - old - x, exactly
-  rest = fabsf(x) < INFINITY ? rest : 0.f;
-  const bool over = above_border(x, rest, A.hi_h, A.hi_l) > 0.f, under = above_border(x, rest, A.lo_h, A.lo_l) < 0.f;
-  const bool far = A.dual && above_border(x, rest, A.dual_h, A.dual_l) > 0.f;
-  const bool clip = (a > 0.f && over) || (a < 0.f && (under || far));
-  const float border = a > 0.f ? 1.f + A.hi : (under ? 1.f - A.lo : A.dual_c);
-  const float ra = a == 0.f ? 0.f : expf(x) * a;      // A = 0: no term, whatever the ratio
+  const float x = __fsub_rn(lp, old);
+  // A rounded x above (below) the border's nearest float is an exact one above (below) the border; where they are
+  // equal, the rests decide.
+  bool over = x > A.hi_h, under = x < A.lo_h, far = x > A.dual_h;
+  if (x == A.hi_h || x == A.lo_h || x == A.dual_h) {
+    const float rest = difference_rest(lp, old, x);
+    over = over || (x == A.hi_h && rest > A.hi_l);
+    under = under || (x == A.lo_h && rest < A.lo_l);
+    far = far || (x == A.dual_h && rest > A.dual_l);
+  }
+  const bool clip = a > 0.f ? over : (a < 0.f && (under || far));
+  const float border = a > 0.f ? A.hi1 : (under ? A.lo1 : A.dual_c);
+  const float ra = a == 0.f ? 0.f : exp2_approx(x * 1.4426950408889634f) * a;     // A = 0: no term, whatever the ratio
   const float obj = clip ? border * a : ra;
   clipped = clip ? 1.f : 0.f;
   kl = 0.f;
   float dk = 0.f;
-  if (A.ref) {
+  if (KL != kNoKl) {
     const float y = lp - ref;
-    if (A.kl_kind == kK1) {
+    if (KL == kK1) {
       kl = y;
       dk = 1.f;
-    } else if (A.kl_kind == kK2) {
+    } else if (KL == kK2) {
       kl = 0.5f * y * y;
       dk = y;
     } else {
-      const float e = expf(-y);
+      const float e = exp2_approx(y * -1.4426950408889634f);
       const bool small = fabsf(y) < 0.5f;
       kl = small ? y * y * exp_tail_series(-y) : e - 1.f + y;      // e^-y - 1 + y
       dk = small ? y - kl : 1.f - e;                               // 1 - e^-y
@@ -431,7 +455,20 @@ __device__ __forceinline__ void policy_token(const PolicyArgs& A, float lp, floa
   d = fmaf(A.kl_coef, dk, clip ? 0.f : -ra);
 }
 
-template <int TEAM, bool VEC>
+// The blocks' partial scalars, joined in block order by one block.
+__device__ __forceinline__ void policy_join(const PolicyArgs& A, int blocks, double* red) {
+  double v[3] = {0.0, 0.0, 0.0};
+  for (int i = threadIdx.x; i < blocks; i += kThreads)
+#pragma unroll
+    for (int j = 0; j < 3; ++j) v[j] += __ldcg(A.part + 3 * i + j);
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    v[j] = team_sum<kThreads>(v[j], red);
+    if (threadIdx.x == 0) A.loss[j] = (float)v[j];
+  }
+}
+
+template <int TEAM, bool VEC, int KL>
 __global__ void __launch_bounds__(kThreads, 4) policy_loss_kernel(const PolicyArgs A) {
   __shared__ double red[kThreads / 32];
   constexpr int kTeams = kThreads / TEAM;
@@ -452,7 +489,14 @@ __global__ void __launch_bounds__(kThreads, 4) policy_loss_kernel(const PolicyAr
     item_range(A.q, s, (int)(it - s * A.q.splits), lo, hi);
     double w = inv_total;
     if (A.per_sequence) {
-      const double n = warp_sum_array(A.sums + s * A.q.splits, A.q.splits, 1);   // every warp of the team
+      double n = 0.0;
+      if (A.sums) {
+        n = warp_sum_array(A.sums + s * A.q.splits, A.q.splits, 1);             // every warp of the team
+      } else if (A.mask) {                    // the mask's second reading, below, finds it in L1
+        n = team_sum<TEAM>(mask_sum<TEAM, VEC>(A.mask, lo, hi, tid), red);
+      } else {
+        n = (double)(hi - lo);
+      }
       w = n != 0.0 ? 1.0 / (n * (double)A.q.S) : 0.0;
     }
     const float wg = (float)w * g;
@@ -467,13 +511,13 @@ __global__ void __launch_bounds__(kThreads, 4) policy_loss_kernel(const PolicyAr
         float lp[4], od[4], rf[4], a[4], l[4], k[4], c[4];
         load4<VEC>(A.logp, t0, lo, hi, lp);
         load4<VEC>(A.old, t0, lo, hi, od);
-        if (A.ref) load4<VEC>(A.ref, t0, lo, hi, rf);
+        if (KL != kNoKl) load4<VEC>(A.ref, t0, lo, hi, rf);
         if (!A.adv_per_seq) load4<VEC>(A.adv, t0, lo, hi, a);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {         // a masked place may hold anything, NaN included
           const bool on = m[j] != 0.f;
-          policy_token(A, on ? lp[j] : 0.f, on ? od[j] : 0.f, on && A.ref ? rf[j] : 0.f,
-                       on ? (A.adv_per_seq ? as : a[j]) : 0.f, l[j], k[j], c[j], d[j]);
+          policy_token<KL>(A, on ? lp[j] : 0.f, on ? od[j] : 0.f, KL != kNoKl && on ? rf[j] : 0.f,
+                           on ? (A.adv_per_seq ? as : a[j]) : 0.f, l[j], k[j], c[j], d[j]);
           d[j] = on ? wg * m[j] * d[j] : 0.f;
         }
         il += (double)fmaf(m[0], l[0], fmaf(m[1], l[1], fmaf(m[2], l[2], m[3] * l[3])));
@@ -495,17 +539,13 @@ __global__ void __launch_bounds__(kThreads, 4) policy_loss_kernel(const PolicyAr
     A.part[3 * blockIdx.x + 1] = sum_k;
     A.part[3 * blockIdx.x + 2] = sum_c;
   }
-  if (last_block(A.counter)) {
-    double v[3] = {0.0, 0.0, 0.0};
-    for (unsigned i = threadIdx.x; i < gridDim.x; i += kThreads)
-#pragma unroll
-      for (int j = 0; j < 3; ++j) v[j] += __ldcg(A.part + 3 * i + j);
-#pragma unroll
-    for (int j = 0; j < 3; ++j) {
-      v[j] = team_sum<kThreads>(v[j], red);
-      if (threadIdx.x == 0) A.loss[j] = (float)v[j];
-    }
-  }
+  if (A.sums && last_block(A.counter)) policy_join(A, gridDim.x, red);
+}
+
+// One block: the scalars of a launch that had nothing before it to zero the counter.
+__global__ void __launch_bounds__(kThreads) policy_finish_kernel(const PolicyArgs A, int blocks) {
+  __shared__ double red[kThreads / 32];
+  policy_join(A, blocks, red);
 }
 
 // out = x g, the gradient of a loss whose unit gradient x was kept.

@@ -193,13 +193,14 @@ class PreferenceLossFunction(torch.autograd.Function):
                                                     average, None, ctx.needs_input_grad[0])
         ctx.save_for_backward(dlogp)
         ctx.mark_non_differentiable(chosen, rejected)
+        ctx.set_materialize_grads(False)
         return loss, chosen, rejected
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad, *_):
         (dlogp,) = ctx.saved_tensors
-        return (_scaled(dlogp, grad),) + (None,) * 8
+        return (None if grad is None else _scaled(dlogp, grad),) + (None,) * 8
 
 
 class PolicyLossFunction(torch.autograd.Function):
@@ -211,13 +212,14 @@ class PolicyLossFunction(torch.autograd.Function):
                                                 ctx.needs_input_grad[0])
         ctx.save_for_backward(dlogp)
         ctx.mark_non_differentiable(kl_mean, clipped)
+        ctx.set_materialize_grads(False)
         return loss, kl_mean, clipped
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad, *_):
         (dlogp,) = ctx.saved_tensors
-        return (_scaled(dlogp, grad),) + (None,) * 11
+        return (None if grad is None else _scaled(dlogp, grad),) + (None,) * 11
 
 
 def preference_loss(logp, ref_logp=None, mask=None, offsets=None, beta: float = 0.1, kind: str = "sigmoid",

@@ -125,15 +125,21 @@ class TokenLogprobsFunction(torch.autograd.Function):
         logp, lse, ent = token_logprobs_forward(H, W, labels, T, entropy)
         ctx.save_for_backward(H, W, labels, lse, ent)
         ctx.T, ctx.chunk = T, chunk
+        ctx.set_materialize_grads(False)
         return (logp, ent) if entropy else logp
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dlogp, dent=None):
+        if dlogp is None and dent is None:
+            return (None,) * 6
         H, W, labels, lse, ent = ctx.saved_tensors
-        dH, dW = token_logprobs_backward(H, W, labels, lse, dlogp.contiguous(), ctx.T, ctx.chunk,
-                                         ent if dent is not None else None,
-                                         dent.contiguous() if dent is not None else None,
+        dlogp = torch.zeros_like(lse) if dlogp is None else dlogp.contiguous()
+        if dent is None:                # the entropy took no part in the loss
+            ent = None
+        else:
+            dent = dent.contiguous()
+        dH, dW = token_logprobs_backward(H, W, labels, lse, dlogp, ctx.T, ctx.chunk, ent, dent,
                                          dW_dtype=W.dtype if ctx.needs_input_grad[1] else None)
         return dH, dW, None, None, None, None
 

@@ -253,9 +253,12 @@ def test_autograd(kd):
     # an expanded (stride 0) upstream gradient, and only one of the two outputs used
     one = torch.ones(300, device="cuda")
     zero = torch.zeros_like(one)
-    want = kd.token_logprobs_backward(Hc.detach(), Wc.detach(), yc, raw[1], one, 0.8, entropy=raw[2], dentropy=zero,
+    want = kd.token_logprobs_backward(Hc.detach(), Wc.detach(), yc, raw[1], one, 0.8, dW_dtype=torch.bfloat16)
+    got = torch.autograd.grad(logp.sum(), (Hc, Wc), retain_graph=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    want = kd.token_logprobs_backward(Hc.detach(), Wc.detach(), yc, raw[1], zero, 0.8, entropy=raw[2], dentropy=one,
                                       dW_dtype=torch.bfloat16)
-    got = torch.autograd.grad(logp.sum(), (Hc, Wc))
+    got = torch.autograd.grad(ent.sum(), (Hc, Wc))
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     # a frozen head
     logp = kd.token_logprobs(Hc, Wc.detach(), yc, T=0.8)
