@@ -12,7 +12,7 @@ LIB_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIB_DIR, "libkdtopkl.so")
 SOURCES = ["kd_topk_kl.cu", "kd_sequence_losses.cu"]
 HEADERS = ["kd_ptx.cuh", "kd_gemm.cuh", "kd_small_kernels.cuh", "kd_schedule.h", "kd_topk_select.cuh",
-           "kd_token_logp.cuh", "kd_sequence_losses.cuh"]
+           "kd_token_logp.cuh", "kd_sequence_losses.cuh", "kd_launch.cuh"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",

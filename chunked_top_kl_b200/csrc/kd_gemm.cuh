@@ -23,6 +23,7 @@
 
 #include <type_traits>
 
+#include "kd_launch.cuh"
 #include "kd_ptx.cuh"
 #include "kd_schedule.h"
 #include "kd_small_kernels.cuh"
@@ -557,6 +558,8 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__
     }
   }
   const uint32_t tmem_base = pipeline_setup<G, PAIR>(L);
+  next_may_start();
+  wait_previous();
 
   // The schedule; a launch over a device-side row count rebuilds it here.
   GemmArgs A = args;

@@ -14,7 +14,7 @@ using namespace kd::seq;
 
 namespace {
 
-constexpr int64_t kSplitItems = 1184;     // items to aim at when few sequences are split (8 blocks per SM)
+constexpr int64_t kSplitItems = 592;      // items to aim at when few sequences are split: one wave, 4 blocks per SM
 constexpr int64_t kTokensPerItem = 4 * kThreads;
 constexpr int64_t kWarpTokens = 192;      // mean length up to which a warp takes a sequence
 
@@ -81,12 +81,16 @@ void two_floats(double v, float* h, float* l) {
 
 int launched() { return cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA; }
 
+template <class K, class... A>
+int next(K kernel, unsigned blocks, cudaStream_t s, A&&... args) {
+  return kd::launch_next(kernel, blocks, (unsigned)kThreads, s, args...) == cudaSuccess ? KD_OK : KD_ERR_CUDA;
+}
+
 template <int TEAM, bool VEC>
 int run_preference(const PrefArgs& A, cudaStream_t s) {
   pref_sums_kernel<TEAM, VEC><<<blocks_for(A.q, TEAM, kSumBlocks), kThreads, 0, s>>>(A);
   if (launched() != KD_OK) return KD_ERR_CUDA;
-  pref_loss_kernel<TEAM, VEC><<<blocks_for(A.q, TEAM, kLossBlocks), kThreads, 0, s>>>(A);
-  return launched();
+  return next(pref_loss_kernel<TEAM, VEC>, blocks_for(A.q, TEAM, kLossBlocks), s, A);
 }
 
 template <int TEAM, bool VEC, int KL>
@@ -96,14 +100,12 @@ int run_policy(PolicyArgs A, cudaStream_t s) {
     A.sums = nullptr;
     policy_loss_kernel<TEAM, VEC, KL><<<blocks, kThreads, 0, s>>>(A);
     if (launched() != KD_OK) return KD_ERR_CUDA;
-    policy_finish_kernel<<<1, kThreads, 0, s>>>(A, blocks);
-    return launched();
+    return next(policy_finish_kernel, 1, s, A, blocks);
   }
   A.sum_blocks = (int)blocks_for(A.q, TEAM, kSumBlocks);
   policy_sums_kernel<TEAM, VEC><<<A.sum_blocks, kThreads, 0, s>>>(A);
   if (launched() != KD_OK) return KD_ERR_CUDA;
-  policy_loss_kernel<TEAM, VEC, KL><<<blocks, kThreads, 0, s>>>(A);
-  return launched();
+  return next(policy_loss_kernel<TEAM, VEC, KL>, blocks, s, A);
 }
 
 template <int TEAM, bool VEC>

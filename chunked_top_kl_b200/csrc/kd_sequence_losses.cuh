@@ -23,6 +23,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "kd_launch.cuh"
+
 namespace kd {
 namespace seq {
 
@@ -184,6 +186,7 @@ struct PrefArgs {
 template <int TEAM, bool VEC>
 __global__ void __launch_bounds__(kThreads, 4) pref_sums_kernel(const PrefArgs A) {
   __shared__ double red[kThreads / 32];
+  next_may_start();
   if (blockIdx.x == 0 && threadIdx.x == 0) *A.counter = 0u;
   constexpr int kTeams = kThreads / TEAM;
   const int tid = threadIdx.x % TEAM;
@@ -254,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 4) pref_loss_kernel(const PrefArgs A
       for (int u = 0; u < kSumUnroll; ++u)
         load_mask4<VEC>(A.mask, (((lo >> 2) + tid) << 2) + 4 * TEAM * u, lo, hi, m[u]);
     float coef = 0.f;
+    wait_previous();                          // for the sums
     if (tid < 32) {
       const bool is_chosen = s < P;
       double r, w, ro, wo;
@@ -261,22 +265,17 @@ __global__ void __launch_bounds__(kThreads, 4) pref_loss_kernel(const PrefArgs A
       seq_ratio(A, is_chosen ? s + P : s - P, ro, wo);
       const double diff = is_chosen ? r - ro : ro - r;
       const double D = A.beta * diff - A.margin;
-      double l, slope;                        // the pair's loss and its derivative in r_chosen
-      if (A.kind == kSigmoid) {
-        l = (1.0 - A.smoothing) * softplus64(-D) + A.smoothing * softplus64(D);
-        slope = A.beta * (1.0 / (1.0 + exp(-D)) - (1.0 - A.smoothing));
-      } else if (A.kind == kHinge) {
-        l = D < 1.0 ? 1.0 - D : (D >= 1.0 ? 0.0 : D);        // NaN stays NaN
-        slope = D < 1.0 ? -A.beta : (D >= 1.0 ? 0.0 : D);
-      } else {
-        const double e = diff - A.margin - 0.5 / A.beta;
-        l = e * e;
-        slope = 2.0 * e;
-      }
+      double slope;                           // the pair loss's derivative in r_chosen
+      const double e = diff - A.margin - 0.5 / A.beta;
+      if (A.kind == kSigmoid) slope = A.beta * (1.0 / (1.0 + exp(-D)) - (1.0 - A.smoothing));
+      else if (A.kind == kHinge) slope = D < 1.0 ? -A.beta : (D >= 1.0 ? 0.0 : D);       // NaN stays NaN
+      else slope = 2.0 * e;
       coef = (float)((is_chosen ? slope : -slope) * w * g / (double)P);
       if (tid == 0 && k == 0) {
         if (is_chosen) {
-          mine += l;
+          if (A.kind == kSigmoid) mine += (1.0 - A.smoothing) * softplus64(-D) + A.smoothing * softplus64(D);
+          else if (A.kind == kHinge) mine += D < 1.0 ? 1.0 - D : (D >= 1.0 ? 0.0 : D);
+          else mine += e * e;
           A.chosen[s] = (float)(A.beta * r);
         } else {
           A.rejected[s - P] = (float)(A.beta * r);
@@ -306,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 4) pref_loss_kernel(const PrefArgs A
       }
     }
   }
+  wait_previous();                            // a block without an item, too: the counter is the first launch's
   if (A.dlogp) zero_outside(A.q, A.dlogp);
   mine = team_sum<kThreads>(mine, red);
   if (threadIdx.x == 0) A.part[blockIdx.x] = mine;
@@ -371,6 +371,7 @@ __device__ __forceinline__ double mask_sum(const float* __restrict__ mask, int l
 template <int TEAM, bool VEC>
 __global__ void __launch_bounds__(kThreads, 8) policy_sums_kernel(const PolicyArgs A) {
   __shared__ double red[kThreads / 32];
+  next_may_start();
   if (blockIdx.x == 0 && threadIdx.x == 0) *A.counter = 0u;
   constexpr int kTeams = kThreads / TEAM;
   const int tid = threadIdx.x % TEAM;
@@ -471,11 +472,13 @@ __device__ __forceinline__ void policy_join(const PolicyArgs& A, int blocks, dou
 template <int TEAM, bool VEC, int KL>
 __global__ void __launch_bounds__(kThreads, 4) policy_loss_kernel(const PolicyArgs A) {
   __shared__ double red[kThreads / 32];
+  next_may_start();
   constexpr int kTeams = kThreads / TEAM;
   const int tid = threadIdx.x % TEAM;
   const int64_t items = A.q.S * A.q.splits;
   const float g = A.grad_loss ? *A.grad_loss : 1.f;
   double inv_total = 0.0;
+  if (A.sums) wait_previous();
   if (!A.per_sequence) {
     double t = 0.0;
     for (int i = threadIdx.x; i < A.sum_blocks; i += kThreads) t += A.total[i];
@@ -545,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, 4) policy_loss_kernel(const PolicyAr
 // One block: the scalars of a launch that had nothing before it to zero the counter.
 __global__ void __launch_bounds__(kThreads) policy_finish_kernel(const PolicyArgs A, int blocks) {
   __shared__ double red[kThreads / 32];
+  wait_previous();
   policy_join(A, blocks, red);
 }
 

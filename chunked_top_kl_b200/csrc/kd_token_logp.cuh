@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(kLabelThreads) label_prep_kernel(const LabelPr
   __shared__ unsigned int s_bad;
   __shared__ unsigned long long s_best, s_dh;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  next_may_start();
   if (t == 0) {
     s_bad = 0u;
     s_best = s_dh = ~0ull;
@@ -77,29 +78,35 @@ __global__ void __launch_bounds__(kLabelThreads) label_prep_kernel(const LabelPr
   for (int64_t base = 0; base < P.N; base += 4 * kLabelThreads) {
     const int64_t n0 = base + 4 * t;
     int lab[4], keep = 0;
+    int64_t y[4];
+    float g[4], h[4];
     unsigned int bad = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      lab[j] = -1;
+    for (int j = 0; j < 4; ++j) {             // all loads first
       const int64_t n = n0 + j;
-      if (n >= P.N) continue;
-      const int64_t y = P.labels_i64 ? static_cast<const int64_t*>(P.labels)[n]
-                                     : (int64_t)static_cast<const int32_t*>(P.labels)[n];
-      bool on = y >= 0 && y < P.V;
-      const bool wrong = y >= P.V;
+      const bool in = n < P.N;
+      y[j] = !in ? -1
+                 : P.labels_i64 ? static_cast<const int64_t*>(P.labels)[n]
+                                : (int64_t) static_cast<const int32_t*>(P.labels)[n];
+      g[j] = in && P.dlogp ? P.dlogp[n] : 0.f;
+      h[j] = in && P.dent ? P.dent[n] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t n = n0 + j;
+      bool on = y[j] >= 0 && y[j] < P.V;
+      const bool wrong = y[j] >= P.V;
       bad += wrong;
       if (P.dlogp) {
-        on = on && (P.dlogp[n] != 0.f || (P.dent && P.dent[n] != 0.f));    // NaN stays in
-      } else if (!on) {
+        on = on && (g[j] != 0.f || h[j] != 0.f);        // NaN stays in
+      } else if (!on && n < P.N) {
         const float v = wrong ? __int_as_float(0x7fc00000) : 0.f;
         P.logp[n] = v;
         P.lse[n] = v;
         if (P.ent) P.ent[n] = v;
       }
-      if (on) {
-        lab[j] = (int)y;
-        ++keep;
-      }
+      lab[j] = on ? (int)y[j] : -1;
+      keep += on;
     }
     int scan = keep;
 #pragma unroll
@@ -174,6 +181,9 @@ __device__ __forceinline__ float dot8(const uint4& x, const uint4& y) {
 // (16-byte vectors, d8 per row), a warp per row.  Rows past the live ones are
 // zero up to the end of the last band of 256, as far as the GEMMs read.
 //
+// Going back, it also clears dH (`clear`; the rows that are left out stay 0)
+// and the pacing counters of the chunk's joint launch.
+//
 // With zlab (the forward pass) each row's label logit H[n] W[lab] is taken on
 // the way, in 64-bit partial sums: it enters the log-probability undiminished,
 // and the tensor cores return a logit of ten some 1e-5 off at d = 2880.  W's
@@ -187,7 +197,13 @@ constexpr int kPadRows = 64;
 __global__ void __launch_bounds__(256)
 gather_live_kernel(const uint4* __restrict__ src, int d8, const int32_t* __restrict__ rowmap,
                    const LiveRows* __restrict__ live, int row0, int C, uint4* __restrict__ dst,
-                   const uint4* __restrict__ W, const int32_t* __restrict__ lab, float* __restrict__ zlab) {
+                   const uint4* __restrict__ W, const int32_t* __restrict__ lab, float* __restrict__ zlab,
+                   uint4* __restrict__ clear, int64_t clear_n, unsigned int* __restrict__ counters, int64_t counters_n) {
+  next_may_start();
+  wait_previous();
+  const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+  for (int64_t i = i0; i < clear_n; i += step) clear[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int64_t i = i0; i < counters_n; i += step) counters[i] = 0u;
   int rows = live->count - row0;
   rows = rows < 0 ? 0 : (rows > C ? C : rows);
   const int64_t room = C > kPadRows ? C : kPadRows, want = ceil_div64(rows, 256) * 256;
@@ -366,6 +382,8 @@ logp_merge_kernel(const float* __restrict__ part_m, const float* __restrict__ pa
                   float* __restrict__ logp, float* __restrict__ lse, float* __restrict__ ent,
                   const Status* __restrict__ status) {
   __shared__ LogpState<ENT> s_part[LANES][ROWS];
+  next_may_start();
+  wait_previous();
   const int rows = live->count, splits = live->raster.splits;
   const int x = threadIdx.x % ROWS, y = threadIdx.x / ROWS;
   const int q = blockIdx.x * ROWS + x;
@@ -459,6 +477,7 @@ template <int NT, bool ENT>
 __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) logp_few_kernel(const FewArgs A) {
   __shared__ int s_tok[kFewTokens], s_lab[kFewTokens];
   __shared__ LogpState<ENT> s_part[kFewWarps][8 * NT];
+  next_may_start();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   // every warp finds the live tokens; block 0 says so to the merge
   int64_t y = -1;
@@ -727,6 +746,8 @@ struct EpiDhPart {
 __global__ void __launch_bounds__(256)
 dh_finish_kernel(const float4* __restrict__ part, int d8, const int32_t* __restrict__ rowmap,
                  const LiveRows* __restrict__ live, int row0, int C, int full_splits, uint4* __restrict__ dH) {
+  next_may_start();
+  wait_previous();
   int rows = live->count - row0;
   rows = rows < 0 ? 0 : (rows > C ? C : rows);
   const int splits = rows == C ? full_splits : live->dh.k_splits;
@@ -780,6 +801,7 @@ struct EpiDwHalf {
 
 // out = bf16(in): the fp32 dW that several chunks added up.
 __global__ void __launch_bounds__(256) round_bf16_kernel(const float4* __restrict__ in, uint2* __restrict__ out, int64_t n4) {
+  wait_previous();
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
     const float4 f = in[i];
     out[i] = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));

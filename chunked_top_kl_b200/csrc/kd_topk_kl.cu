@@ -202,7 +202,7 @@ cudaError_t launch_gemm(int slot, int dev, int groups, const CUtensorMap& ta0, c
                         const CUtensorMap& to0, const CUtensorMap& ta1, const CUtensorMap& tb1,
                         const CUtensorMap& to1, const GemmArgs& args,
                         const typename P0::Epi::Params& ep0, const typename P1::Epi::Params& ep1,
-                        cudaStream_t s) {
+                        cudaStream_t s, bool next = false) {
   using G = Geo<PAIR, P0::Epi::kStaging || P1::Epi::kStaging>;
   auto kern = gemm_tc_kernel<P0, P1, PAIR>;
   if (dev >= 0 && dev < kMaxDevices && !g_dev[dev].attr_set[slot]) {
@@ -215,13 +215,15 @@ cudaError_t launch_gemm(int slot, int dev, int groups, const CUtensorMap& ta0, c
   cfg.blockDim = dim3(GEMM_THREADS, 1, 1);
   cfg.dynamicSmemBytes = G::SMEM_BYTES;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = PAIR ? 2 : 1;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // `next`: see kd_launch.cuh
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = next ? 2 : 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ta0, tb0, to0, ta1, tb1, to1, args, ep0, ep1);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
@@ -232,14 +234,14 @@ template <class P0>
 cudaError_t launch_one(int slot, int dev, int groups, const CUtensorMap& ta, const CUtensorMap& tb,
                        const CUtensorMap& to, const ProbArgs& pa, Status* status,
                        const typename P0::Epi::Params& ep, cudaStream_t s, DynRows dyn = DynRows{},
-                       unsigned int* wave_sync = nullptr) {
+                       unsigned int* wave_sync = nullptr, bool next = false) {
   GemmArgs a{};
   a.prob[0] = pa;
   a.status = status;
   a.dyn = dyn;
   a.wave_sync = wave_sync;
   EpiNone::Params none{};
-  return launch_gemm<P0, NoProb, kPair>(slot, dev, groups, ta, tb, to, ta, tb, to, a, ep, none, s);
+  return launch_gemm<P0, NoProb, kPair>(slot, dev, groups, ta, tb, to, ta, tb, to, a, ep, none, s, next);
 }
 
 // Problem 0 round-robin, problem 1 dealt to even out the groups' total K
@@ -932,10 +934,10 @@ int logp_forward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, 
   float* zlab = at<float>(ws, L.off_zlab);
   const unsigned copy_blocks = (unsigned)(device_sms(dev) * 8);
   const int64_t want = ceil_div(N > kPadRows ? N : kPadRows, 8);
-  gather_live_kernel<<<(unsigned)(want < copy_blocks ? want : copy_blocks), 256, 0, s>>>(
-      static_cast<const uint4*>(H), (int)(d / 8), lp.rowmap, live, 0, (int)N, static_cast<uint4*>(hc),
-      static_cast<const uint4*>(W), lp.lab, zlab);
-  if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
+  if (launch_next(gather_live_kernel, (unsigned)(want < copy_blocks ? want : copy_blocks), 256u, s,
+                  static_cast<const uint4*>(H), (int)(d / 8), lp.rowmap, live, 0, (int)N, static_cast<uint4*>(hc),
+                  static_cast<const uint4*>(W), lp.lab, zlab, nullptr, 0, nullptr, 0) != cudaSuccess)
+    return KD_ERR_CUDA;
 
   CUtensorMap tmH, tmW;
   if (!make_map(&tmH, hc, d, N > kPadRows ? N : kPadRows, d, BK, BM) || !make_map(&tmW, W, d, V, d, BK, GeoP::B_ROWS)) return KD_ERR_CUDA;
@@ -953,11 +955,12 @@ int logp_forward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, 
   ep.part_g = part + 2 * L.slots;
   ep.part_t = part + 3 * L.slots;
   if (launch_one<ProbLogp<ENT>>(ENT ? 5 : 4, dev, lp.groups, tmH, tmW, tmH, a, lp.status, ep, s,
-                                DynRows{&live->count, 0, (int)N, &live->raster}, wave) != cudaSuccess)
+                                DynRows{&live->count, 0, (int)N, &live->raster}, wave, true) != cudaSuccess)
     return KD_ERR_CUDA;
-  logp_merge_kernel<ENT, 32, 8><<<(unsigned)ceil_div(N, 32), 256, 0, s>>>(
-      ep.part_m, ep.part_s, ep.part_t, ep.part_g, live, lp.rowmap, zlab, ep.zl2, kLog2e / T, logp, lse, ent, lp.status);
-  return cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;
+  return launch_next(logp_merge_kernel<ENT, 32, 8>, (unsigned)ceil_div(N, 32), 256u, s, ep.part_m, ep.part_s, ep.part_t,
+                     ep.part_g, live, lp.rowmap, zlab, ep.zl2, kLog2e / T, logp, lse, ent, lp.status) == cudaSuccess
+             ? KD_OK
+             : KD_ERR_CUDA;
 }
 
 template <bool ENT>
@@ -1000,9 +1003,10 @@ int logp_forward_few(const void* H, const void* W, const void* labels, int label
   }
   kern<<<grid, kFewThreads, (size_t)few_smem(N, d), s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
-  logp_merge_kernel<ENT, 1, 256><<<(unsigned)N, 256, 0, s>>>(a.part_m, a.part_s, a.part_t, a.part_g, a.live, a.rowmap,
-                                                            a.zlab, a.zl2, a.zl2, logp, lse, ent, a.status);
-  return cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA;
+  return launch_next(logp_merge_kernel<ENT, 1, 256>, (unsigned)N, 256u, s, a.part_m, a.part_s, a.part_t, a.part_g, a.live,
+                     a.rowmap, a.zlab, a.zl2, a.zl2, logp, lse, ent, a.status) == cudaSuccess
+             ? KD_OK
+             : KD_ERR_CUDA;
 }
 
 template <bool ENT>
@@ -1026,7 +1030,6 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
   lp.dw_units = dw_units;
   lp.part_rows = L.part_rows;
   lp.joint_groups = groups;
-  if (cudaMemsetAsync(dH, 0, sizeof(__nv_bfloat16) * (size_t)N * d, s) != cudaSuccess) return KD_ERR_CUDA;
   label_prep_kernel<<<1, kLabelThreads, 0, s>>>(lp);
   if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
 
@@ -1036,9 +1039,6 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
   void* hc = at<char>(ws, L.off_hc);
   float* part32 = at<float>(ws, L.off_part32);
   unsigned int* jwave = at<unsigned int>(ws, L.off_jwave);
-  if (with_dW && cudaMemsetAsync(jwave, 0, sizeof(unsigned int) * (size_t)L.jwave_per_chunk * ceil_div(N, C), s) !=
-                     cudaSuccess)
-    return KD_ERR_CUDA;
   CUtensorMap tmHk, tmWk, tmWmn, tmHmn, tmDH, tmDW;
   if (!make_map(&tmHk, hc, d, C, d, BK, BM) || !make_map(&tmWk, W, d, V, d, BK, GeoP::B_ROWS) ||
       !make_map(&tmWmn, W, d, V, d, 64, BK) || !make_map(&tmHmn, hc, d, C, d, 64, BK) ||
@@ -1056,9 +1056,11 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
     const DynRows dyn{&live->count, (int)c0, (int)Cc, &live->raster, &live->dh};
     const int64_t want = ceil_div(Cc, 8);
     const unsigned blocks = (unsigned)(want < copy_blocks ? want : copy_blocks);
-    gather_live_kernel<<<blocks, 256, 0, s>>>(static_cast<const uint4*>(H), (int)(d / 8), lp.rowmap, live, (int)c0,
-                                              (int)Cc, static_cast<uint4*>(hc), nullptr, nullptr, nullptr);
-    if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
+    unsigned int* wave = with_dW ? jwave + (size_t)(c0 / C) * L.jwave_per_chunk : nullptr;
+    if (launch_next(gather_live_kernel, blocks, 256u, s, static_cast<const uint4*>(H), (int)(d / 8), lp.rowmap, live,
+                    (int)c0, (int)Cc, static_cast<uint4*>(hc), nullptr, nullptr, nullptr, static_cast<uint4*>(dH),
+                    c0 == 0 ? N * (d / 8) : 0, wave, wave ? L.jwave_per_chunk : 0) != cudaSuccess)
+      return KD_ERR_CUDA;
 
     ProbArgs az{};
     az.raster = forward_raster(ceil_div(Cc, GeoP::TILE_M), n_tiles, dz_groups, 0, 0, kMaxDzSplits);
@@ -1075,8 +1077,8 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
     ez.ent = ent;
     ez.dlogp = dlogp;
     ez.dent = dent;
-    if (launch_one<ProbDlogp<ENT>>(ENT ? 7 : 6, dev, dz_groups, tmHk, tmWk, tmZk, az, lp.status, ez, s, dyn) !=
-        cudaSuccess)
+    if (launch_one<ProbDlogp<ENT>>(ENT ? 7 : 6, dev, dz_groups, tmHk, tmWk, tmZk, az, lp.status, ez, s, dyn, nullptr,
+                                   true) != cudaSuccess)
       return KD_ERR_CUDA;
 
     // dH and dW of the chunk in one launch, as in the distillation loss's backward pass; dH alone without a dW
@@ -1095,35 +1097,39 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
     cudaError_t e;
     if (!with_dW) {
       EpiNone::Params none{};
-      e = launch_gemm<ProbDhPart, NoProb, kPair>(9, dev, groups, tmZk, tmWmn, tmDH, tmZk, tmWmn, tmDH, j, eh, none, s);
+      e = launch_gemm<ProbDhPart, NoProb, kPair>(9, dev, groups, tmZk, tmWmn, tmDH, tmZk, tmWmn, tmDH, j, eh, none, s,
+                                              true);
     } else {
       j.prob[1].raster = tile_raster(ceil_div(V, GeoP::TILE_M), dh_cols, false);
       j.prob[1].num_kb = (int)ceil_div(Cc, BK);
       j.prob[1].dyn_role = 2;
       plan_second_problem(j, groups);
       if (j.prob[1].num_kb >= (plan.wide_cols ? kPaceKBlocksWide : kPaceKBlocks))
-        j.wave_sync = jwave + (size_t)(c0 / C) * L.jwave_per_chunk;
+        j.wave_sync = wave;
       if (half_store) {
         j.prob[1].dyn_zero_fill = 1;
         EpiDwHalf::Params eb{};
-        e = launch_gemm<ProbDhPart, ProbDwHalf, kPair>(8, dev, groups, tmZk, tmWmn, tmDH, tmZmn, tmHmn, tmDW, j, eh, eb, s);
+        e = launch_gemm<ProbDhPart, ProbDwHalf, kPair>(8, dev, groups, tmZk, tmWmn, tmDH, tmZmn, tmHmn, tmDW, j, eh, eb, s,
+                                                   true);
       } else {
         EpiDw::Params ew{};
         ew.accumulate = ((accumulate_dW && !rounds) || c0 > 0) ? 1 : 0;
         j.prob[1].dyn_zero_fill = ew.accumulate ? 0 : 1;
-        e = launch_gemm<ProbDhPart, ProbDw, kPair>(10, dev, groups, tmZk, tmWmn, tmDH, tmZmn, tmHmn, tmDW, j, eh, ew, s);
+        e = launch_gemm<ProbDhPart, ProbDw, kPair>(10, dev, groups, tmZk, tmWmn, tmDH, tmZmn, tmHmn, tmDW, j, eh, ew, s,
+                                              true);
       }
     }
     if (e != cudaSuccess) return KD_ERR_CUDA;
     const int64_t finish = ceil_div(Cc * (d / 8), 256);
-    dh_finish_kernel<<<(unsigned)(finish < copy_blocks ? finish : copy_blocks), 256, 0, s>>>(
-        reinterpret_cast<const float4*>(part32), (int)(d / 8), lp.rowmap, live, (int)c0, (int)Cc, plan.k_splits,
-        static_cast<uint4*>(dH));
-    if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
+    if (launch_next(dh_finish_kernel, (unsigned)(finish < copy_blocks ? finish : copy_blocks), 256u, s,
+                    reinterpret_cast<const float4*>(part32), (int)(d / 8), lp.rowmap, live, (int)c0, (int)Cc,
+                    plan.k_splits, static_cast<uint4*>(dH)) != cudaSuccess)
+      return KD_ERR_CUDA;
   }
   if (rounds) {
-    round_bf16_kernel<<<copy_blocks, 256, 0, s>>>(static_cast<const float4*>(dWacc), static_cast<uint2*>(dW), V * d / 4);
-    if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
+    if (launch_next(round_bf16_kernel, copy_blocks, 256u, s, static_cast<const float4*>(dWacc), static_cast<uint2*>(dW),
+                    V * d / 4) != cudaSuccess)
+      return KD_ERR_CUDA;
   }
   return KD_OK;
 }
