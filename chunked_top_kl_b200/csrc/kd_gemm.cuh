@@ -74,13 +74,15 @@ struct ProbArgs {
   int wide_cols;        // > 0: wide units (Prob WIDE): its 256-column tiles; the raster counts pairs of them
   int k_splits;         // Prob KSPLIT: K ranges per tile (at least 1); raster column n is column
   int k_cols;           // n % k_cols of K range n / k_cols
+  int min_blocks;       // a unit's cost is at least that of this many K blocks (its epilogue's)
 };
 
 // K blocks of MMA work per unit of a problem, the joint schedule's cost: a
 // wide unit's K block runs two MMA blocks (one per column tile).  A problem
 // declared WIDE runs wide units when the launch sets wide_cols.
 KD_HD int64_t unit_cost(const ProbArgs& pa) {
-  const int64_t kb = pa.k_splits > 1 ? ceil_div64(pa.num_kb, pa.k_splits) : pa.num_kb;
+  int64_t kb = pa.k_splits > 1 ? ceil_div64(pa.num_kb, pa.k_splits) : pa.num_kb;
+  if (kb < pa.min_blocks) kb = pa.min_blocks;
   return (int64_t)pa.raster.tiles_per_split * kb * (pa.wide_cols > 0 ? 2 : 1);
 }
 

@@ -151,8 +151,12 @@ KD_HD int64_t logp_units_bound(int64_t N) { return kLogpMaxSplits + logp_part_sl
 // parts are added up afterwards in order.  Chosen is the cut, and wide units
 // or not (see wide_pays), with the least work of the busiest group, counting
 // for each range the parts' bytes, written and read again (8 a value; a K block
-// of a group, a quarter of a microsecond, is about 2^20 bytes of traffic).
+// of a group, a quarter of a microsecond, is about 2^20 bytes of traffic).  A dW
+// tile of few K blocks costs what its epilogue does, about kDwMinBlocks of them
+// (backward pass of 193 / 30 tokens at V = 32,001, d = 1000: 103 / 133 us
+// without, 91 / 88 us with 8, 101 / 98 us with 12).
 constexpr int kMaxDhSplits = 64;
+constexpr int kDwMinBlocks = 8;
 
 struct DhPlan {
   int wide_cols;   // 256-column tiles when units are wide, else 0
@@ -170,7 +174,8 @@ KD_HD int64_t dh_cost(int64_t bands, int64_t n_cols, int64_t d, int64_t k0, int6
   if (k_splits > kMaxDhSplits || k_splits > k0 || (k_splits > 1 && bands * 256 * k_splits > part_rows) ||
       (wide && n_cols < 2))
     return -1;
-  const int64_t avg = ceil_div64(bands * n_cols * k0 + U1 * k1, groups);
+  const int64_t dw = U1 * (k1 < kDwMinBlocks ? kDwMinBlocks : k1);
+  const int64_t avg = ceil_div64(bands * n_cols * k0 + dw, groups);
   const int64_t units = bands * k_splits * (wide ? ceil_div64(n_cols, 2) : n_cols);
   const int64_t own = ceil_div64(units, groups) * ceil_div64(k0, k_splits) * (wide ? 2 : 1);
   return (own > avg ? own : avg) + ((k_splits * bands * 256 * d * 8) >> 20);

@@ -1103,6 +1103,7 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
       j.prob[1].raster = tile_raster(ceil_div(V, GeoP::TILE_M), dh_cols, false);
       j.prob[1].num_kb = (int)ceil_div(Cc, BK);
       j.prob[1].dyn_role = 2;
+      j.prob[1].min_blocks = kDwMinBlocks;
       plan_second_problem(j, groups);
       if (j.prob[1].num_kb >= (plan.wide_cols ? kPaceKBlocksWide : kPaceKBlocks))
         j.wave_sync = wave;
