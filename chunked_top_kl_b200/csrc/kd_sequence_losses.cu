@@ -2,6 +2,7 @@
 // kd_policy_loss): argument checks, workspace layout, how the sequences are
 // cut into items, and the launches.
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -86,26 +87,63 @@ int next(K kernel, unsigned blocks, cudaStream_t s, A&&... args) {
   return kd::launch_next(kernel, blocks, (unsigned)kThreads, s, args...) == cudaSuccess ? KD_OK : KD_ERR_CUDA;
 }
 
+// SMs of the current device.
+int current_sms() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (!n) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// Whether the phases are one launch: a call whose time is the host's, every
+// item of which has a team of its own among the blocks that the GPU holds at once.
+bool one_launch(const Sequences& q, int team, unsigned blocks) {
+  return q.N <= kOneLaunchTokens && (int64_t)blocks * (kThreads / team) >= q.S * q.splits && blocks <= (unsigned)(kResident * current_sms());
+}
+
+template <class K, class A>
+int cooperative(K kernel, unsigned blocks, cudaStream_t s, const A& args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess ? launched() : KD_ERR_CUDA;
+}
+
 template <int TEAM, bool VEC>
 int run_preference(const PrefArgs& A, cudaStream_t s) {
+  const unsigned blocks = blocks_for(A.q, TEAM, kLossBlocks);
+  if (one_launch(A.q, TEAM, blocks)) return cooperative(pref_one_kernel<TEAM, VEC>, blocks, s, A);
   pref_sums_kernel<TEAM, VEC><<<blocks_for(A.q, TEAM, kSumBlocks), kThreads, 0, s>>>(A);
   if (launched() != KD_OK) return KD_ERR_CUDA;
-  return next(pref_loss_kernel<TEAM, VEC>, blocks_for(A.q, TEAM, kLossBlocks), s, A);
+  return next(pref_loss_kernel<TEAM, VEC>, blocks, s, A);
 }
 
 template <int TEAM, bool VEC, int KL>
 int run_policy(PolicyArgs A, cudaStream_t s) {
-  const int blocks = (int)blocks_for(A.q, TEAM, kLossBlocks);
-  if (A.per_sequence && A.q.splits == 1) {
-    A.sums = nullptr;
-    policy_loss_kernel<TEAM, VEC, KL><<<blocks, kThreads, 0, s>>>(A);
+  const unsigned blocks = blocks_for(A.q, TEAM, kLossBlocks);
+  const bool own_sums = A.per_sequence && A.q.splits == 1;
+  if (own_sums) A.sums = nullptr;
+  if (one_launch(A.q, TEAM, blocks)) return cooperative(policy_one_kernel<TEAM, VEC, KL>, blocks, s, A);
+  if (own_sums) {
+    policy_loss_kernel<TEAM, VEC, KL><<<blocks, kThreads, 0, s>>>(A, 0);
     if (launched() != KD_OK) return KD_ERR_CUDA;
-    return next(policy_finish_kernel, 1, s, A, blocks);
+    return next(policy_finish_kernel, 1, s, A, (int)blocks);
   }
-  A.sum_blocks = (int)blocks_for(A.q, TEAM, kSumBlocks);
-  policy_sums_kernel<TEAM, VEC><<<A.sum_blocks, kThreads, 0, s>>>(A);
+  const unsigned sum_blocks = blocks_for(A.q, TEAM, kSumBlocks);
+  policy_sums_kernel<TEAM, VEC><<<sum_blocks, kThreads, 0, s>>>(A);
   if (launched() != KD_OK) return KD_ERR_CUDA;
-  return next(policy_loss_kernel<TEAM, VEC, KL>, blocks, s, A);
+  return next(policy_loss_kernel<TEAM, VEC, KL>, blocks, s, A, (int)sum_blocks);
 }
 
 template <int TEAM, bool VEC>
