@@ -242,6 +242,9 @@ __device__ __forceinline__ void seq_ratio(const PrefArgs& A, int64_t s, double& 
   r *= w;
 }
 
+// w v, and 0 for w = 0 whatever v (a pair so far apart that v is infinite).
+__device__ __forceinline__ double share(double w, double v) { return w != 0.0 ? w * v : 0.0; }
+
 __device__ __forceinline__ double softplus64(double v) { return (v > 0.0 ? v : 0.0) + log1p(exp(-fabs(v))); }
 
 // The second phase, up to the block's partial loss.
@@ -280,7 +283,7 @@ __device__ __forceinline__ void pref_losses(const PrefArgs& A, double* red) {
       coef = (float)((is_chosen ? slope : -slope) * w * g / (double)P);
       if (tid == 0 && k == 0) {
         if (is_chosen) {
-          if (A.kind == kSigmoid) mine += (1.0 - A.smoothing) * softplus64(-D) + A.smoothing * softplus64(D);
+          if (A.kind == kSigmoid) mine += share(1.0 - A.smoothing, softplus64(-D)) + share(A.smoothing, softplus64(D));
           else if (A.kind == kHinge) mine += D < 1.0 ? 1.0 - D : (D >= 1.0 ? 0.0 : D);
           else mine += e * e;
           A.chosen[s] = (float)(A.beta * r);
@@ -367,8 +370,8 @@ __global__ void __launch_bounds__(kThreads, kResident) pref_one_kernel(const Pre
 //
 // Whether a token is clipped is decided on the exact difference x, against
 // log(1 + hi), log(1 - lo) and log c, and not on a rounded exponential.  e^x and
-// the KL term are taken in 32 bits (ex2.approx: 2^-22); e^-y - 1 + y, which
-// cancels for small y, by its series for |y| < 1/2.  Tokens are computed
+// the KL term are taken in 32 bits; e^-y - 1 + y, which cancels for small y, by
+// its series for |y| < 1/2.  Tokens are computed
 // without branches, masked ones on zeros: four at a time in flight instead of
 // one behind the other.
 
@@ -422,12 +425,6 @@ __device__ __forceinline__ void policy_sums(const PolicyArgs& A, double* red) {
   if (threadIdx.x == 0) A.total[blockIdx.x] = all;
 }
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // (e^x - 1 - x) / x^2 for |x| < 1/2: sum_k x^k / (k + 2)!, k = 0..8 (the next term is below 2^-31 of it).
 __device__ __forceinline__ float exp_tail_series(float x) {
   float p = 1.f / 3628800.f;
@@ -463,7 +460,7 @@ __device__ __forceinline__ void policy_token(const PolicyArgs& A, float lp, floa
   }
   const bool clip = a > 0.f ? over : (a < 0.f && (under || far));
   const float border = a > 0.f ? A.hi1 : (under ? A.lo1 : A.dual_c);
-  const float ra = a == 0.f ? 0.f : exp2_approx(x * 1.4426950408889634f) * a;     // A = 0: no term, whatever the ratio
+  const float ra = a == 0.f ? 0.f : expf(x) * a;     // A = 0: no term, whatever the ratio
   const float obj = clip ? border * a : ra;
   clipped = clip ? 1.f : 0.f;
   kl = 0.f;
@@ -477,7 +474,7 @@ __device__ __forceinline__ void policy_token(const PolicyArgs& A, float lp, floa
       kl = 0.5f * y * y;
       dk = y;
     } else {
-      const float e = exp2_approx(y * -1.4426950408889634f);
+      const float e = expf(-y);
       const bool small = fabsf(y) < 0.5f;
       kl = small ? y * y * exp_tail_series(-y) : e - 1.f + y;      // e^-y - 1 + y
       dk = small ? y - kl : 1.f - e;                               // 1 - e^-y

@@ -177,55 +177,130 @@ __device__ __forceinline__ float dot8(const uint4& x, const uint4& y) {
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
+// What the dZ epilogue needs of a row: dZ / scale = p (a + b u) with
+// u = z zl2 - bias off the label, `label` at it.
+struct RowCoef {
+  float bias, a, b, label;
+};
+
+// The backward pass's share of gather_live_kernel.
+struct RowScales {
+  const float *lse, *ent, *dlogp, *dent;   // ent and dent null without an entropy gradient
+  float zs;                 // 1 / T
+  RowCoef* coef;            // [C]
+  float* scale;             // [C]
+  uint4* scaled;            // [C][d8] H rows times their scale; null when no dW is wanted
+  uint4* clear;             // dH, cleared: the rows that are left out stay 0
+  int64_t clear_n;
+  unsigned int* counters;   // the joint launch's pacing counters, cleared
+  int64_t counters_n;
+};
+
+// Row n's factors. dZ is formed and rounded to bf16 per row as dZ / scale, with
+// a scale that makes the label's entry exactly 1 or -1: it is the largest, and
+// its rounding error would be a common factor of the token's whole dH row.  dH
+// is multiplied by the scale in fp32, and dW = dZ^T H takes it with H, whose
+// elements round independently.  With pl = p at the label, from the exact logit:
+//   without an entropy gradient  scale = -g (1 - pl) / T, dZ / scale = p / (1 - pl)
+//   (1 - pl folded into the exponent), -1 at the label;
+//   with one, a = -(g + h ent) / T, b = -h ln 2 / T, the label's entry
+//   L = (g (1 - pl) - h pl (log pl + ent)) / T is the scale unless it is small
+//   beside |g| + |h| (then that is, and L / scale is rounded as the others are).
+__device__ __forceinline__ RowCoef row_coef(const RowScales& B, int n, float zy, float& scale) {
+  RowCoef c;
+  const float logp = fmaf(zy, B.zs, -B.lse[n]), g = B.dlogp[n] * B.zs;
+  const float om = -expm1f(logp);
+  c.bias = B.lse[n] * kLog2e;
+  if (!B.dent) {
+    const float room = om < 9.31e-10f ? 9.31e-10f : om;       // 2^-30: 1 - pl of a label whose p rounds to 1; NaN stays
+    scale = -g * room;
+    c.bias += log2f(room);
+    c.a = c.b = 0.f;
+    c.label = -1.f;
+    return c;
+  }
+  const float h = B.dent[n] * B.zs, ent = B.ent[n], base = fabsf(g) + fabsf(h);
+  const float L = g * om - h * (1.f - om) * (logp + ent);
+  const bool own = fabsf(L) > base * 9.77e-4f;                 // 2^-10
+  scale = own ? L : base;
+  c.a = -fmaf(h, ent, g) / scale;
+  c.b = -h * kLn2 / scale;
+  c.label = own ? 1.f : L / scale;
+  return c;
+}
+
+__device__ __forceinline__ uint32_t scale2(uint32_t x, float s) {
+  const float lo = __uint_as_float(x << 16) * s, hi = __uint_as_float(x & 0xffff0000u) * s;
+  return pack_bf16x2(lo, hi);
+}
+
 // Rows [row0, row0 + C) of the live list: dst[r] = src[rowmap[row0 + r]]
 // (16-byte vectors, d8 per row), a warp per row.  Rows past the live ones are
 // zero up to the end of the last band of 256, as far as the GEMMs read.
 //
-// Going back, it also clears dH (`clear`; the rows that are left out stay 0)
-// and the pacing counters of the chunk's joint launch.
-//
-// With zlab (the forward pass) each row's label logit H[n] W[lab] is taken on
-// the way, in 64-bit partial sums: it enters the log-probability undiminished,
-// and the tensor cores return a logit of ten some 1e-5 off at d = 2880.  W's
-// rows are read beside H's, 2 d more bytes a row.
+// Each row's label logit H[n] W[lab] is taken on the way, in 64-bit partial
+// sums: it enters the log-probability undiminished, and the tensor cores return
+// a logit of ten some 1e-5 off at d = 2880.  W's rows are read beside H's, 2 d
+// more bytes a row.  The forward pass keeps it (zlab); going back, the row's
+// scale and coefficients come from it.
 //
 // Of the first rows, kPadRows are written even when fewer are live: loads of a
 // band with a row or two made the one-token product 1.4 times slower (294 us
 // against 207 us at d = 2880, 1.07 GB of W) than those of 64 rows.
 constexpr int kPadRows = 64;
 
+template <bool BACKWARD>
 __global__ void __launch_bounds__(256)
 gather_live_kernel(const uint4* __restrict__ src, int d8, const int32_t* __restrict__ rowmap,
                    const LiveRows* __restrict__ live, int row0, int C, uint4* __restrict__ dst,
                    const uint4* __restrict__ W, const int32_t* __restrict__ lab, float* __restrict__ zlab,
-                   uint4* __restrict__ clear, int64_t clear_n, unsigned int* __restrict__ counters, int64_t counters_n) {
+                   const RowScales B) {
   next_may_start();
   wait_previous();
-  const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
-  for (int64_t i = i0; i < clear_n; i += step) clear[i] = make_uint4(0u, 0u, 0u, 0u);
-  for (int64_t i = i0; i < counters_n; i += step) counters[i] = 0u;
+  if (BACKWARD) {
+    const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+    for (int64_t i = i0; i < B.clear_n; i += step) B.clear[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int64_t i = i0; i < B.counters_n; i += step) B.counters[i] = 0u;
+  }
   int rows = live->count - row0;
   rows = rows < 0 ? 0 : (rows > C ? C : rows);
   const int64_t room = C > kPadRows ? C : kPadRows, want = ceil_div64(rows, 256) * 256;
   const int64_t end = want < room ? want : room;
   const int lane = threadIdx.x & 31;
   for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < end; r += (int64_t)gridDim.x * 8) {
+    uint4* to = dst + (size_t)r * d8;
+    uint4* scaled = BACKWARD && B.scaled ? B.scaled + (size_t)r * d8 : nullptr;
     if (r >= rows) {
-      for (int j = lane; j < d8; j += 32) dst[(size_t)r * d8 + j] = make_uint4(0u, 0u, 0u, 0u);
+      for (int j = lane; j < d8; j += 32) {
+        to[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (scaled) scaled[j] = make_uint4(0u, 0u, 0u, 0u);
+      }
       continue;
     }
-    const uint4* from = src + (size_t)rowmap[row0 + r] * d8;
-    const uint4* w = zlab ? W + (size_t)lab[row0 + r] * d8 : nullptr;
+    const int n = rowmap[row0 + r];
+    const uint4 *from = src + (size_t)n * d8, *w = W + (size_t)lab[row0 + r] * d8;
     double z = 0.0;
     for (int j = lane; j < d8; j += 32) {
       const uint4 h = from[j];
-      dst[(size_t)r * d8 + j] = h;
-      if (w) z += (double)dot8(h, w[j]);
+      to[j] = h;
+      z += (double)dot8(h, w[j]);
     }
-    if (w) {
-      z = warp_sum_d(z);
+    z = warp_sum_d(z);
+    if (!BACKWARD) {
       if (lane == 0) zlab[row0 + r] = (float)z;
+      continue;
     }
+    float scale;
+    const RowCoef c = row_coef(B, n, (float)z, scale);
+    if (lane == 0) {
+      B.coef[r] = c;
+      B.scale[r] = scale;
+    }
+    if (scaled)
+      for (int j = lane; j < d8; j += 32) {
+        const uint4 h = from[j];
+        scaled[j] = make_uint4(scale2(h.x, scale), scale2(h.y, scale), scale2(h.z, scale), scale2(h.w, scale));
+      }
   }
 }
 
@@ -628,49 +703,29 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) logp_few_kernel(
   }
 }
 
-// Backward, per chunk: dZ in bf16 for the chunk's live rows (row-major, ldz
-// columns), stored as EpiDz stores it.  With u = z zl2 - lse log2(e), p = 2^u
-// and the factor 1 / T in g and h:
-//   without ENT  dZ = c (p - 1[v = y]), c = -g: |c| is folded into the
-//                exponent and the sign applied to the packed pairs;
-//   with ENT     dZ = p (a + b u) + g 1[v = y], a = -(g + h ent), b = -h ln 2.
-// The label's term is added before the rounding to bf16: p - 1 of a confident
-// token is small, and a rounded p would leave little of it.
+// Backward, per chunk: dZ over the row's scale (see row_coef) in bf16 for the
+// chunk's live rows (row-major, ldz columns), stored as EpiDz stores it.  With
+// u = z zl2 - bias and p = 2^u: p itself without an entropy gradient (ENT), else
+// p (a + b u); the label's entry is set, not computed.
 template <bool ENT>
 struct EpiDlogp {
   static constexpr bool kStaging = true;
   struct Params {
     int row0;              // live-list index of chunk row 0
     int V;
-    float zl2, zs;         // log2(e) / T (times accumulation_gain) and 1 / T
-    const int32_t *rowmap, *lab;
-    const float *lse, *ent, *dlogp, *dent;
+    float zl2;             // log2(e) / T (times accumulation_gain)
+    const int32_t* lab;
+    const RowCoef* coef;
   };
-  float bias, a, b, add;
-  uint32_t sgn;
+  RowCoef c;
   int label;
 
   __device__ __forceinline__ void begin_unit(const Params& P, int r, int, int, const EpiCtx& cx) {
-    bias = 1e30f;            // rows past the live ones: p = 0 and a finite u
-    a = b = add = 0.f;
-    sgn = 0u;
+    c = RowCoef{1e30f, 0.f, 0.f, 0.f};        // rows past the live ones: p = 0 and a finite u
     label = -1;
     if (r < cx.rows_valid) {
-      const int n = P.rowmap[P.row0 + r];
+      c = P.coef[r];
       label = P.lab[P.row0 + r];
-      const float g = P.dlogp[n] * P.zs;
-      bias = P.lse[n] * kLog2e;
-      if (ENT) {
-        const float h = P.dent[n] * P.zs;
-        a = -fmaf(h, P.ent[n], g);
-        b = -h * kLn2;
-        add = g;
-      } else {
-        const float c = fabsf(g);
-        sgn = g > 0.f ? 0x80008000u : 0u;
-        bias -= log2f(c);
-        add = -c;
-      }
     }
   }
   __device__ __forceinline__ void end_unit(const Params&, int, int) {}
@@ -684,8 +739,8 @@ struct EpiDlogp {
       __syncwarp();
       tmem_ld_32x32b_x64(taddr + j * 64, v);
       const int c0 = n * BN + j * 64;
-      const float2 zl2v = make_float2(zl2, zl2), nb = make_float2(-bias, -bias);
-      const float2 av = make_float2(a, a), bv = make_float2(b, b);
+      const float2 zl2v = make_float2(zl2, zl2), nb = make_float2(-c.bias, -c.bias);
+      const float2 av = make_float2(c.a, c.a), bv = make_float2(c.b, c.b);
 #pragma unroll
       for (int i = 0; i < 64; i += 2) {
         const float2 u = __ffma2_rn(make_float2(v[i], v[i + 1]), zl2v, nb);
@@ -703,15 +758,11 @@ struct EpiDlogp {
       if (__any_sync(0xffffffffu, (unsigned)off < 64u)) {     // a label in this group (rare)
 #pragma unroll
         for (int i = 0; i < 64; ++i)
-          if (i == off) v[i] += add;
+          if (i == off) v[i] = c.label;
       }
       uint32_t w[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-      if (!ENT && sgn) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) w[i] ^= sgn;
-      }
       stage_store(cx, out, c0, cx.row_base, w, false);
     }
   }
@@ -741,11 +792,12 @@ struct EpiDhPart {
   }
 };
 
-// dH[token] = bf16(sum over the K ranges, in order) for the chunk's live rows;
-// eight values a thread.  `full` is the plan of a chunk that is live throughout.
+// dH[token] = bf16(scale * sum over the K ranges, in order) for the chunk's live
+// rows; eight values a thread.  `full` is the plan of a chunk that is live throughout.
 __global__ void __launch_bounds__(256)
 dh_finish_kernel(const float4* __restrict__ part, int d8, const int32_t* __restrict__ rowmap,
-                 const LiveRows* __restrict__ live, int row0, int C, int full_splits, uint4* __restrict__ dH) {
+                 const LiveRows* __restrict__ live, const float* __restrict__ scale, int row0, int C, int full_splits,
+                 uint4* __restrict__ dH) {
   next_may_start();
   wait_previous();
   int rows = live->count - row0;
@@ -763,8 +815,10 @@ dh_finish_kernel(const float4* __restrict__ part, int d8, const int32_t* __restr
       a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
       b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
     }
+    const float s = scale[r];
     dH[(size_t)rowmap[row0 + r] * d8 + j] =
-        make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+        make_uint4(pack_bf16x2(s * a.x, s * a.y), pack_bf16x2(s * a.z, s * a.w), pack_bf16x2(s * b.x, s * b.y),
+                   pack_bf16x2(s * b.z, s * b.w));
   }
 }
 

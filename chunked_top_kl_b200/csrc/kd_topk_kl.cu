@@ -857,7 +857,7 @@ using ProbDlogp = Prob<EpiDlogp<ENT>, false, false, kL2EvictLast, kL2Normal>;
 struct LogpLayout {
   size_t off_status = 0, off_live = 0, off_rowmap = 0, off_lab = 0;
   size_t off_part = 0, off_wave = 0, off_zlab = 0, off_hc = 0;         // forward
-  size_t off_jwave = 0, off_dz = 0, off_part32 = 0, off_dw32 = 0;      // backward
+  size_t off_jwave = 0, off_dz = 0, off_coef = 0, off_scale = 0, off_hs = 0, off_part32 = 0, off_dw32 = 0;   // backward
   int64_t slots = 0, C = 0, ldz = 0, jwave_per_chunk = 0, part_rows = 0;
   size_t total = 0;
 };
@@ -886,6 +886,9 @@ LogpLayout make_logp_layout(int64_t N, int64_t d, int64_t V, int64_t chunk, bool
     L.off_jwave = take(sizeof(unsigned int) * (size_t)L.jwave_per_chunk * ceil_div(n, L.C));
     L.off_dz = take(2 * (size_t)L.C * L.ldz);
     L.off_hc = take(2 * (size_t)(L.C > kPadRows ? L.C : kPadRows) * d);
+    L.off_hs = take(2 * (size_t)(L.C > kPadRows ? L.C : kPadRows) * d);
+    L.off_coef = take(sizeof(RowCoef) * (size_t)L.C);
+    L.off_scale = take(sizeof(float) * (size_t)L.C);
     L.off_part32 = take(sizeof(float) * (size_t)L.part_rows * d);
     if (half_dW && n > L.C) L.off_dw32 = take(sizeof(float) * (size_t)V * d);
   }
@@ -934,9 +937,9 @@ int logp_forward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, 
   float* zlab = at<float>(ws, L.off_zlab);
   const unsigned copy_blocks = (unsigned)(device_sms(dev) * 8);
   const int64_t want = ceil_div(N > kPadRows ? N : kPadRows, 8);
-  if (launch_next(gather_live_kernel, (unsigned)(want < copy_blocks ? want : copy_blocks), 256u, s,
+  if (launch_next(gather_live_kernel<false>, (unsigned)(want < copy_blocks ? want : copy_blocks), 256u, s,
                   static_cast<const uint4*>(H), (int)(d / 8), lp.rowmap, live, 0, (int)N, static_cast<uint4*>(hc),
-                  static_cast<const uint4*>(W), lp.lab, zlab, nullptr, 0, nullptr, 0) != cudaSuccess)
+                  static_cast<const uint4*>(W), lp.lab, zlab, RowScales{}) != cudaSuccess)
     return KD_ERR_CUDA;
 
   CUtensorMap tmH, tmW;
@@ -1037,11 +1040,14 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
   const bool half_store = half_dW && !rounds;
   __nv_bfloat16* dz = at<__nv_bfloat16>(ws, L.off_dz);
   void* hc = at<char>(ws, L.off_hc);
+  void* hs = at<char>(ws, L.off_hs);
+  RowCoef* coef = at<RowCoef>(ws, L.off_coef);
+  float* scale = at<float>(ws, L.off_scale);
   float* part32 = at<float>(ws, L.off_part32);
   unsigned int* jwave = at<unsigned int>(ws, L.off_jwave);
   CUtensorMap tmHk, tmWk, tmWmn, tmHmn, tmDH, tmDW;
   if (!make_map(&tmHk, hc, d, C, d, BK, BM) || !make_map(&tmWk, W, d, V, d, BK, GeoP::B_ROWS) ||
-      !make_map(&tmWmn, W, d, V, d, 64, BK) || !make_map(&tmHmn, hc, d, C, d, 64, BK) ||
+      !make_map(&tmWmn, W, d, V, d, 64, BK) || !make_map(&tmHmn, hs, d, C, d, 64, BK) ||
       !make_map(&tmDH, part32, d, L.part_rows, d, 32, BM, true))
     return KD_ERR_CUDA;
   if (with_dW && !(half_store ? make_map(&tmDW, dWacc, d, V, d, 64, BM) : make_map(&tmDW, dWacc, d, V, d, 32, BM, true)))
@@ -1057,9 +1063,11 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
     const int64_t want = ceil_div(Cc, 8);
     const unsigned blocks = (unsigned)(want < copy_blocks ? want : copy_blocks);
     unsigned int* wave = with_dW ? jwave + (size_t)(c0 / C) * L.jwave_per_chunk : nullptr;
-    if (launch_next(gather_live_kernel, blocks, 256u, s, static_cast<const uint4*>(H), (int)(d / 8), lp.rowmap, live,
-                    (int)c0, (int)Cc, static_cast<uint4*>(hc), nullptr, nullptr, nullptr, static_cast<uint4*>(dH),
-                    c0 == 0 ? N * (d / 8) : 0, wave, wave ? L.jwave_per_chunk : 0) != cudaSuccess)
+    RowScales rs{lse, ent, dlogp, dent, 1.0f / T, coef, scale, with_dW ? static_cast<uint4*>(hs) : nullptr,
+                 static_cast<uint4*>(dH), c0 == 0 ? N * (d / 8) : 0, wave, wave ? L.jwave_per_chunk : 0};
+    if (launch_next(gather_live_kernel<true>, blocks, 256u, s, static_cast<const uint4*>(H), (int)(d / 8), lp.rowmap, live,
+                    (int)c0, (int)Cc, static_cast<uint4*>(hc), static_cast<const uint4*>(W), lp.lab, nullptr, rs) !=
+        cudaSuccess)
       return KD_ERR_CUDA;
 
     ProbArgs az{};
@@ -1070,13 +1078,8 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
     ez.row0 = (int)c0;
     ez.V = (int)V;
     ez.zl2 = (float)(1.4426950408889634 / T * accumulation_gain(d));
-    ez.zs = 1.0f / T;
-    ez.rowmap = lp.rowmap;
     ez.lab = lp.lab;
-    ez.lse = lse;
-    ez.ent = ent;
-    ez.dlogp = dlogp;
-    ez.dent = dent;
+    ez.coef = coef;
     if (launch_one<ProbDlogp<ENT>>(ENT ? 7 : 6, dev, dz_groups, tmHk, tmWk, tmZk, az, lp.status, ez, s, dyn, nullptr,
                                    true) != cudaSuccess)
       return KD_ERR_CUDA;
@@ -1123,7 +1126,7 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
     if (e != cudaSuccess) return KD_ERR_CUDA;
     const int64_t finish = ceil_div(Cc * (d / 8), 256);
     if (launch_next(dh_finish_kernel, (unsigned)(finish < copy_blocks ? finish : copy_blocks), 256u, s,
-                    reinterpret_cast<const float4*>(part32), (int)(d / 8), lp.rowmap, live, (int)c0, (int)Cc,
+                    reinterpret_cast<const float4*>(part32), (int)(d / 8), lp.rowmap, live, scale, (int)c0, (int)Cc,
                     plan.k_splits, static_cast<uint4*>(dH)) != cudaSuccess)
       return KD_ERR_CUDA;
   }

@@ -298,8 +298,9 @@ int kd_token_logp_forward(const void* H, const void* W, const void* labels, int 
  *   dZ[n,v] = (1 / T) (dlogp[n] (1[v = y[n]] - p[n,v])
  *                      - dentropy[n] p[n,v] (log p[n,v] + entropy[n]))
  *   dH = dZ W (bf16 [N][d], overwritten),  dW = dZ^T H
- * with p recomputed from lse, `chunk` tokens at a time; dZ is rounded to bf16
- * before the two products.  Tokens without a valid label and tokens whose
+ * with p recomputed from lse, `chunk` tokens at a time.  Before the two
+ * products dZ is rounded to bf16, each row over a scale that makes the label's
+ * entry exact; dH takes the scale in fp32, dW with H (rounded to bf16 again).  Tokens without a valid label and tokens whose
  * upstream gradients are 0 are left out (their dH rows are 0).  dW is fp32
  * [V][d] (overwritten, or added to with accumulate_dW = 1), or bf16 [V][d]
  * with dW_bf16 = 1 (overwritten; rounded once, after the sum over all

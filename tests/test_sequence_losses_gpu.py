@@ -258,6 +258,25 @@ def test_policy_far_ratios(kd):
             assert kl == pytest.approx(oracle.policy_loss(lp, lp, zero, ref, None, [(0, lp.size)])[1], rel=64 * U)
 
 
+def test_preference_of_pairs_infinitely_far_apart(kd):
+    """A chosen or rejected answer of probability 0: the pair's loss is 0 or infinite, its slope 0 or -beta, never NaN
+    (without smoothing the second term has no part); other pairs keep their gradients."""
+    lp = torch.tensor([-1.0, -2.0, -3.0, -1.0, -2.0, -3.0], device="cuda")
+    off = torch.arange(7, device="cuda", dtype=torch.int32)
+    base = kd.preference_loss_forward_backward(lp, None, None, off, beta=0.5)
+    lp[4] = float("-inf")                                  # pair 1: D = +inf
+    loss, chosen, rejected, g = kd.preference_loss_forward_backward(lp, None, None, off, beta=0.5)
+    want = 2 / 3 * math.log(2.0)
+    assert float(loss) == pytest.approx(want, rel=4 * U) and float(rejected[1]) == -math.inf
+    assert g[1] == 0 and g[4] == 0 and torch.equal(g[[0, 2, 3, 5]], base[3][[0, 2, 3, 5]])
+    lp[4], lp[1] = -2.0, float("-inf")                     # pair 1: D = -inf
+    loss, chosen, rejected, g = kd.preference_loss_forward_backward(lp, None, None, off, beta=0.5)
+    assert float(loss) == math.inf and g[1].item() == pytest.approx(-0.5 / 3, rel=4 * U) and g[4] == -g[1]
+    for kind, want, slope in (("hinge", math.inf, -0.5 / 3), ("ipo", math.inf, -math.inf)):
+        loss, _, _, g = kd.preference_loss_forward_backward(lp, None, None, off, beta=0.5, kind=kind)
+        assert float(loss) == want and g[1].item() == pytest.approx(slope, rel=4 * U)
+
+
 def test_upstream_gradient_and_autograd(kd):
     x = _inputs("short_odd", 41)
     off = torch.tensor(x["offsets"], device="cuda", dtype=torch.int32)
