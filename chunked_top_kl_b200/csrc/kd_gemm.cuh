@@ -72,9 +72,10 @@ struct ProbArgs {
   int dyn_bands_fastest;
   int dyn_zero_fill;    // role 2 with no live rows: still write the (zero) output tiles
   int wide_cols;        // > 0: wide units (Prob WIDE): its 256-column tiles; the raster counts pairs of them
-  int k_splits;         // Prob KSPLIT: K ranges per tile (at least 1); raster column n is column
-  int k_cols;           // n % k_cols of K range n / k_cols
+  int k_splits;         // Prob KSPLIT: K ranges per tile (at least 1) of
+  int k_bands;          // k_bands bands; raster band m is band m % k_bands of K range m / k_bands
   int min_blocks;       // a unit's cost is at least that of this many K blocks (its epilogue's)
+  int by_loads;         // count a unit's operand loads (kBlockLoads, kWideBlockLoads a K block) as its cost
 };
 
 // K blocks of MMA work per unit of a problem, the joint schedule's cost: a
@@ -83,7 +84,8 @@ struct ProbArgs {
 KD_HD int64_t unit_cost(const ProbArgs& pa) {
   int64_t kb = pa.k_splits > 1 ? ceil_div64(pa.num_kb, pa.k_splits) : pa.num_kb;
   if (kb < pa.min_blocks) kb = pa.min_blocks;
-  return (int64_t)pa.raster.tiles_per_split * kb * (pa.wide_cols > 0 ? 2 : 1);
+  const int one = pa.by_loads ? kBlockLoads : 1, wide = pa.by_loads ? kWideBlockLoads : 2;
+  return (int64_t)pa.raster.tiles_per_split * kb * (pa.wide_cols > 0 ? wide : one);
 }
 
 // A launch over rows whose number is known only on the device (a chunk of the
@@ -132,18 +134,23 @@ __device__ __forceinline__ void wave_barrier(unsigned int* counter, unsigned int
 template <class G, bool HAS_P1>
 __device__ __forceinline__ void apply_live_rows(GemmArgs& a, int rows, int ngroups) {
   const Raster* given = a.dyn.raster;
+  if (a.dyn.plan)
+    for (int p = 0; p < (HAS_P1 ? 2 : 1); ++p) a.prob[p].by_loads = dh_by_loads(ceil_div64(rows, G::TILE_M));
 #pragma unroll
   for (int p = 0; p < (HAS_P1 ? 2 : 1); ++p) {
     ProbArgs& pa = a.prob[p];
     if (pa.dyn_role == 1) {
-      if (a.dyn.plan && rows > 0 && rows != a.dyn.chunk) {
-        const DhPlan c = *a.dyn.plan;
+      const int64_t bands = ceil_div64(rows, G::TILE_M);
+      int parts = 1;
+      if (a.dyn.plan) {
+        DhPlan c{pa.wide_cols, pa.k_splits, pa.raster.n_tiles};
+        if (rows > 0 && rows != a.dyn.chunk) c = *a.dyn.plan;
         pa.wide_cols = c.wide_cols;
-        pa.k_splits = c.k_splits;
-        pa.k_cols = c.k_cols;
-        pa.raster.n_tiles = c.k_cols * c.k_splits;
+        pa.k_splits = parts = c.k_splits;
+        pa.k_bands = (int)bands;
+        pa.raster.n_tiles = c.k_cols;
       }
-      pa.raster = tile_raster(ceil_div64(rows, G::TILE_M), pa.raster.n_tiles, pa.dyn_bands_fastest != 0);
+      pa.raster = tile_raster(bands * parts, pa.raster.n_tiles, pa.dyn_bands_fastest != 0);
     } else if (given && (pa.dyn_role == 3 || pa.dyn_role == 4)) {
       if (rows == 0) pa.raster.num_units = 0;
       else if (pa.dyn_role == 4 || rows != a.dyn.chunk) pa.raster = *given;
@@ -162,7 +169,9 @@ __device__ __forceinline__ void apply_live_rows(GemmArgs& a, int rows, int ngrou
 // Compile-time description of a problem: its epilogue, operand majorness,
 // the L2 eviction priority of each operand's loads (L2Hint), whether its units
 // are wide, and whether a tile's K blocks may be cut into ranges that separate
-// units compute (KSPLIT; the epilogue gets the range's index).  A wide unit computes two neighbouring 256-column tiles of
+// units compute (KSPLIT).  The ranges are raster bands: those of one range follow
+// one another, so that its part of B is read once for all bands, and the output
+// rows of a range's bands lie behind those of the range before.  A wide unit computes two neighbouring 256-column tiles of
 // one band (column tiles 2n and 2n + 1 for raster column n) into the two
 // accumulators at once, so each K block's A tile is loaded once for both:
 // three quarters of the operand bytes per MMA block of a one-tile unit.  The
@@ -225,7 +234,6 @@ struct EpiCtx {
   bool issuer;
   uint32_t seq;
   int rows_valid;       // live rows of a DynRows launch, else -1
-  int part_row0;        // KSPLIT: rows of the K ranges before this one (whole bands)
 };
 
 // Writes one 128-byte segment per thread (its row) into the next staging
@@ -373,19 +381,18 @@ __device__ __forceinline__ void next_acc(RoleState& st) {
   if (st.acc == 0) st.acc_phase ^= 1u;
 }
 
-// K blocks [kb0, kb1) and K range of raster column n; n becomes the column within the range.
+// K blocks [kb0, kb1) of raster band m; the band of the operand's rows.
 template <class P>
-__device__ __forceinline__ int unit_krange(const ProbArgs& pa, int& n, int& kb0, int& kb1) {
+__device__ __forceinline__ int unit_krange(const ProbArgs& pa, int m, int& kb0, int& kb1) {
   kb0 = 0;
   kb1 = pa.num_kb;
   if constexpr (P::KSPLIT) {
-    const int part = n / pa.k_cols;
-    n -= part * pa.k_cols;
+    const int part = m / pa.k_bands;
     kb0 = (int)((int64_t)pa.num_kb * part / pa.k_splits);
     kb1 = (int)((int64_t)pa.num_kb * (part + 1) / pa.k_splits);
-    return part;
+    return m - part * pa.k_bands;
   }
-  return 0;
+  return m;
 }
 
 // Column tiles of raster column n: [first, first + count).
@@ -408,10 +415,11 @@ __device__ __forceinline__ bool produce_unit(const Smem<G>& L, RoleState& st, ui
                                              const CUtensorMap* tB, int u) {
   int m, split, n0, n1;
   decode_unit(pa.raster, u, m, split, n0, n1);
+  int kb0, kb1;
+  m = unit_krange<P>(pa, m, kb0, kb1);
   for (int n = n0; n < n1; ++n) {
-    int c0, nc, kb0, kb1, col = n;
-    unit_krange<P>(pa, col, kb0, kb1);
-    unit_cols<P>(pa, col, c0, nc);
+    int c0, nc;
+    unit_cols<P>(pa, n, c0, nc);
     for (int kb = kb0; kb < kb1; ++kb) {
       // stage 1: A and the first column tile's B; stage 2 (wide units): the second B
       for (int h = 0; h < nc; ++h) {
@@ -440,10 +448,11 @@ __device__ __forceinline__ bool mma_unit(const Smem<G>& L, RoleState& st, uint32
   constexpr uint32_t idesc = idesc_bf16_f32(G::TILE_M, BN, P::A_MN, P::B_MN);
   int m, split, n0, n1;
   decode_unit(pa.raster, u, m, split, n0, n1);
+  int kb0, kb1;
+  unit_krange<P>(pa, m, kb0, kb1);
   for (int n = n0; n < n1; ++n) {
-    int c0, nc, kb0, kb1, col = n;
-    unit_krange<P>(pa, col, kb0, kb1);
-    unit_cols<P>(pa, col, c0, nc);
+    int c0, nc;
+    unit_cols<P>(pa, n, c0, nc);
     // the unit's accumulators: this one and, for a wide unit, the next
     RoleState a2 = st;
     next_acc(a2);
@@ -498,9 +507,8 @@ __device__ __forceinline__ bool epi_unit(const Smem<G>& L, RoleState& st, uint32
   cx.row_base = m * G::TILE_M + (int)rank * BM;
   epi.begin_unit(ep, grow, split, n0, cx);
   for (int n = n0; n < n1; ++n) {
-    int c0, nc, kb0, kb1, col = n;
-    cx.part_row0 = unit_krange<P>(pa, col, kb0, kb1) * pa.raster.m_tiles * G::TILE_M;
-    unit_cols<P>(pa, col, c0, nc);
+    int c0, nc;
+    unit_cols<P>(pa, n, c0, nc);
     for (int h = 0; h < nc; ++h) {      // a wide unit's two tiles, one accumulator each
       // One outcome for all 128 epilogue threads: tcgen05.ld needs whole
       // warps and the store path synchronises the four warps.
@@ -528,7 +536,6 @@ __device__ __forceinline__ EpiCtx make_epi_ctx(uint32_t staging) {
   cx.seq = 0;
   cx.row_base = 0;
   cx.rows_valid = -1;
-  cx.part_row0 = 0;
   return cx;
 }
 

@@ -149,19 +149,28 @@ KD_HD int64_t logp_units_bound(int64_t N) { return kLogpMaxSplits + logp_part_sl
 // millisecond at V = 128,256), so a few bands of rows leave most groups idle:
 // its K blocks are then cut into ranges, each a unit of its own, whose fp32
 // parts are added up afterwards in order.  Chosen is the cut, and wide units
-// or not (see wide_pays), with the least work of the busiest group, counting
-// for each range the parts' bytes, written and read again (8 a value; a K block
-// of a group, a quarter of a microsecond, is about 2^20 bytes of traffic).  A dW
-// tile of few K blocks costs what its epilogue does, about kDwMinBlocks of them
-// (backward pass of 193 / 30 tokens at V = 32,001, d = 1000: 103 / 133 us
-// without, 91 / 88 us with 8, 101 / 98 us with 12).
+// or not (see wide_pays), with the least work of the busiest group.  Below
+// kLoadBands bands the launch is bound by the operands' loads, so work is counted
+// in them: a K block of a tile loads four quarters, of a wide unit (two tiles that
+// share the band's A) six; else in products, eight.  Each range adds its parts' bytes, written and read again
+// (8 a value; a K block, half a microsecond here, is about 2^20 of them).  A dW
+// tile of few K blocks costs what its epilogue does, kDwMinBlocks of them.
+// Backward pass with products as the measure / with loads (us): 200 tokens at
+// V = 201,088, d = 2880: 1077 / 1045; 1000 tokens at V = 128,256, d = 2048:
+// 1540 / 1410, dH alone 1075 / 920; a policy step of 967 labelled tokens at
+// V = 201,088: 4345 / 4010.  With 20 bands loads as the measure make the forward
+// and backward pass of 8,192 tokens 2 % slower (18.2 / 18.6 ms).
+// kDwMinBlocks: 30 tokens at V = 32,001, d = 1000: 133 us without, 88 us with 8.
 constexpr int kMaxDhSplits = 64;
+constexpr int kLoadBands = 8;
+KD_HD bool dh_by_loads(int64_t bands) { return bands < kLoadBands; }
 constexpr int kDwMinBlocks = 8;
+constexpr int kBlockLoads = 4, kWideBlockLoads = 6;
 
 struct DhPlan {
   int wide_cols;   // 256-column tiles when units are wide, else 0
   int k_splits;    // K ranges
-  int k_cols;      // raster columns of one range
+  int k_cols;      // raster columns
 };
 
 // Rows (of d floats) that hold the parts of a chunk of C rows: the ranges of
@@ -174,11 +183,12 @@ KD_HD int64_t dh_cost(int64_t bands, int64_t n_cols, int64_t d, int64_t k0, int6
   if (k_splits > kMaxDhSplits || k_splits > k0 || (k_splits > 1 && bands * 256 * k_splits > part_rows) ||
       (wide && n_cols < 2))
     return -1;
-  const int64_t dw = U1 * (k1 < kDwMinBlocks ? kDwMinBlocks : k1);
-  const int64_t avg = ceil_div64(bands * n_cols * k0 + dw, groups);
-  const int64_t units = bands * k_splits * (wide ? ceil_div64(n_cols, 2) : n_cols);
-  const int64_t own = ceil_div64(units, groups) * ceil_div64(k0, k_splits) * (wide ? 2 : 1);
-  return (own > avg ? own : avg) + ((k_splits * bands * 256 * d * 8) >> 20);
+  const int64_t loads = !wide ? kBlockLoads : dh_by_loads(bands) ? kWideBlockLoads : 2 * kBlockLoads,
+                cols = wide ? ceil_div64(n_cols, 2) : n_cols;
+  const int64_t dw = U1 * (k1 < kDwMinBlocks ? kDwMinBlocks : k1) * kBlockLoads;
+  const int64_t avg = ceil_div64(bands * cols * k0 * loads + dw, groups);
+  const int64_t own = ceil_div64(bands * k_splits * cols, groups) * ceil_div64(k0, k_splits) * loads;
+  return (own > avg ? own : avg) + ((k_splits * bands * 256 * d * 8 * kBlockLoads) >> 20);
 }
 
 // Candidates in the order of preference: fewer ranges first, then wide units.

@@ -787,7 +787,7 @@ struct EpiDhPart {
       uint32_t w[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
-      stage_store(cx, out, n * BN + j * 32, cx.part_row0 + cx.row_base, w, false);
+      stage_store(cx, out, n * BN + j * 32, cx.row_base, w, false);
     }
   }
 };

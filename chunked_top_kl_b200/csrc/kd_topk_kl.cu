@@ -1090,12 +1090,13 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
     j.dyn = dyn;
     const int64_t dh_bands = ceil_div(Cc, GeoP::TILE_M), k1 = with_dW ? ceil_div(Cc, BK) : 0;
     const DhPlan plan = dh_plan(dh_bands, dh_cols, d, ceil_div(V, BK), dw_units, k1, groups, L.part_rows);
-    j.prob[0].raster = tile_raster(dh_bands, (int64_t)plan.k_cols * plan.k_splits, false);
+    j.prob[0].raster = tile_raster(dh_bands * plan.k_splits, plan.k_cols, false);
     j.prob[0].num_kb = (int)ceil_div(V, BK);
     j.prob[0].dyn_role = 1;
     j.prob[0].wide_cols = plan.wide_cols;
     j.prob[0].k_splits = plan.k_splits;
-    j.prob[0].k_cols = plan.k_cols;
+    j.prob[0].k_bands = (int)dh_bands;
+    j.prob[0].by_loads = j.prob[1].by_loads = dh_by_loads(dh_bands);
     EpiDhPart::Params eh{};
     cudaError_t e;
     if (!with_dW) {
