@@ -4,8 +4,9 @@
 // next_may_start, and waits in wait_previous until it has finished and its
 // writes are visible.  Each kernel of a chain calls wait_previous before it
 // touches anything that a kernel writes, so that the last one's end is the
-// end of all.  The first of a call is an ordinary launch.  Both calls do
-// nothing in a kernel that was launched the ordinary way.
+// end of all.  The first of a call is an ordinary launch, and the last does not
+// let another start before its end: what follows the call may be anyone's.
+// Both calls do nothing in a kernel that was launched the ordinary way.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -152,9 +152,10 @@ KD_HD int64_t logp_units_bound(int64_t N) { return kLogpMaxSplits + logp_part_sl
 // or not (see wide_pays), with the least work of the busiest group.  Below
 // kLoadBands bands the launch is bound by the operands' loads, so work is counted
 // in them: a K block of a tile loads four quarters, of a wide unit (two tiles that
-// share the band's A) six; else in products, eight.  Each range adds its parts' bytes, written and read again
-// (8 a value; a K block, half a microsecond here, is about 2^20 of them).  A dW
-// tile of few K blocks costs what its epilogue does, kDwMinBlocks of them.
+// share the band's A) six; else in products, eight.  Each range adds its parts'
+// bytes, written and read again (8 a value; a K block, half a microsecond here,
+// is about 2^20 of them).  A dW tile of few K blocks costs what its epilogue does,
+// kDwMinBlocks of them.
 // Backward pass with products as the measure / with loads (us): 200 tokens at
 // V = 201,088, d = 2880: 1077 / 1045; 1000 tokens at V = 128,256, d = 2048:
 // 1540 / 1410, dH alone 1075 / 920; a policy step of 967 labelled tokens at

@@ -12,8 +12,9 @@
 // team sums its sequence's mask and finds it in L1 when it reads it again.
 //
 // Up to kOneLaunchTokens tokens, when all items find a team at once, the phases
-// are one cooperative launch with a grid barrier between them, else two
-// launches (the second waits for the first's end only where it needs the sums).
+// are one cooperative launch (which CUDA starts only when all of its blocks are
+// resident) with a grid barrier between them, else two launches (the second waits
+// for the first's end only where it needs the sums).
 // One launch saves the host 2.5 us, and costs the GPU 3 us with 256 blocks:
 // calls back to back take 20.3 against 22.6 us (preference, 190 thousand
 // tokens), 21.7 against 24.2 (policy, half a million), 41.3 against 34.8
@@ -580,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 8) policy_sums_kernel(const PolicyAr
 template <int TEAM, bool VEC, int KL>
 __global__ void __launch_bounds__(kThreads, 5) policy_loss_kernel(const PolicyArgs A, int sum_blocks) {
   __shared__ double red[kThreads / 32];
-  next_may_start();
+  if (!A.sums) next_may_start();              // policy_finish_kernel
   policy_losses<TEAM, VEC, KL>(A, sum_blocks, red);
   if (A.sums && last_block(A.counter)) policy_join(A, gridDim.x, red);
 }

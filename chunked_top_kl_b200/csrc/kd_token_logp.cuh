@@ -307,10 +307,11 @@ gather_live_kernel(const uint4* __restrict__ src, int d8, const int32_t* __restr
 // Forward: running scaled maximum and sum-exp over the unit's vocabulary
 // columns, the label's logit, and with ENT the sum of e u that the entropy
 // needs.  In log2 units, u_v = z_v zl2 - mb with zl2 = log2(e) / T (times
-// accumulation_gain) and mb = max z * zl2 as rounded: s = sum 2^u and t = sum 2^u u (u <= 0, so t
-// does not cancel).  A new maximum shifts u by delta = mb_old - mb_new:
-// t <- 2^delta (t + delta s), s <- 2^delta s.  Partials (mb, s, t, label
-// logit) per live row and column range; columns >= V are taken as -1e30.
+// accumulation_gain) and mb = max z * zl2 as rounded: s = sum 2^u and
+// t = sum 2^u u (u <= 0, so t does not cancel).  A new maximum shifts u by
+// delta = mb_old - mb_new: t <- 2^delta (t + delta s), s <- 2^delta s.
+// Partials (mb, s, t, label logit) per live row and column range; columns >= V
+// are taken as -1e30.
 template <bool ENT>
 struct EpiLogp {
   static constexpr bool kStaging = false;
@@ -457,7 +458,6 @@ logp_merge_kernel(const float* __restrict__ part_m, const float* __restrict__ pa
                   float* __restrict__ logp, float* __restrict__ lse, float* __restrict__ ent,
                   const Status* __restrict__ status) {
   __shared__ LogpState<ENT> s_part[LANES][ROWS];
-  next_may_start();
   wait_previous();
   const int rows = live->count, splits = live->raster.splits;
   const int x = threadIdx.x % ROWS, y = threadIdx.x / ROWS;
@@ -513,9 +513,12 @@ logp_merge_kernel(const float* __restrict__ part_m, const float* __restrict__ pa
 // times two; as every k counts alike, A and B take the same eight in the same
 // order.  H lies in shared memory in the order of the loads (few_smem bytes: a
 // d that does not fit goes to the GEMM); read through L1 it was pushed out by
-// the stream of W (206 us instead of 195 us for a token, 316 instead of 223 for nine).  The
-// running softmax state is as in EpiLogp, a thread holding two tokens (per eight) over the rows it meets;
-// warps, then blocks (through the partials, one range per block) are joined.
+// the stream of W (206 us instead of 195 us for a token, 316 instead of 223 for
+// nine).  The running softmax state is as in EpiLogp, a thread holding two tokens
+// (per eight) over the rows it meets; warps, then blocks (through the partials,
+// one range per block) are joined.  195 us for a token at V = 201,088, d = 2880
+// (5.9 TB/s), 223 for sixteen, where the GEMM takes 228; seventeen and more took
+// 440 us here.
 //
 // Every kFewBatch k blocks the products start from zero and are added up in
 // fp32 with rounding: sums so short need no accumulation_gain.
@@ -798,7 +801,6 @@ __global__ void __launch_bounds__(256)
 dh_finish_kernel(const float4* __restrict__ part, int d8, const int32_t* __restrict__ rowmap,
                  const LiveRows* __restrict__ live, const float* __restrict__ scale, int row0, int C, int full_splits,
                  uint4* __restrict__ dH) {
-  next_may_start();
   wait_previous();
   int rows = live->count - row0;
   rows = rows < 0 ? 0 : (rows > C ? C : rows);

@@ -896,11 +896,14 @@ LogpLayout make_logp_layout(int64_t N, int64_t d, int64_t V, int64_t chunk, bool
   return L;
 }
 
-// T is bounded so that a padding column's -1e30 stays finite in log2 units.
+// T is bounded so that a padding column's -1e30 stays finite in log2 units, N
+// and V so that a row or column a tile or two past the last one is still an int.
+constexpr int64_t kMaxLogpIndex = (int64_t(1) << 31) - (int64_t(1) << 16);
+
 int logp_checks(int64_t N, int64_t d, int64_t V, float T, int64_t chunk) {
   if (N < 0 || d <= 0 || V <= 0 || chunk <= 0 || !(T > 0.f)) return KD_ERR_INVALID_ARG;
   if (d % 8 != 0 || T < 1e-6f || T > 1e6f) return KD_ERR_UNSUPPORTED;
-  if (N >= (int64_t(1) << 31) || V >= (int64_t(1) << 31) || d >= (int64_t(1) << 24)) return KD_ERR_UNSUPPORTED;
+  if (N > kMaxLogpIndex || V > kMaxLogpIndex || d >= (int64_t(1) << 24)) return KD_ERR_UNSUPPORTED;
   return KD_OK;
 }
 

@@ -149,5 +149,7 @@ def token_logprobs(H, W, labels, T: float = 1.0, chunk: int = LOGP_CHUNK, entrop
     (logp, entropy), both differentiable, with ``entropy``: see
     token_logprobs_forward.  dW comes in W's bf16 (rounded once, at the end),
     and is not computed for a frozen head; call ``token_logprobs_backward`` for
-    an fp32 gradient."""
+    an fp32 gradient, and the two raw calls to capture a step in a CUDA graph
+    (an autograd backward pass runs on the streams of its leaves' other graphs
+    too, which a capture does not allow)."""
     return TokenLogprobsFunction.apply(H, W, labels, T, chunk, entropy)

@@ -277,7 +277,7 @@ int kd_teacher_topk(const void* Ht, const void* Wt, int64_t N, int64_t d, int64_
 
 /* Label log-probabilities under the head, for losses on labels, preferences
  * and rewards.  For labels y (int32 [N], or int64 when labels_i64 is 1) and
- * temperature T (1e-6 <= T <= 1e6) writes, per token,
+ * temperature T (1e-6 <= T <= 1e6; N and V at most 2^31 - 2^16) writes, per token,
  *   z = H W^T / T,  lse[n] = log sum_v exp(z[n,v])
  *   logp[n] = z[n, y[n]] - lse[n]
  *   entropy[n] = lse[n] - sum_v softmax(z[n])[v] z[n,v]    (entropy may be NULL)
@@ -304,7 +304,7 @@ int kd_token_logp_forward(const void* H, const void* W, const void* labels, int 
  * upstream gradients are 0 are left out (their dH rows are 0).  dW is fp32
  * [V][d] (overwritten, or added to with accumulate_dW = 1), or bf16 [V][d]
  * with dW_bf16 = 1 (overwritten; rounded once, after the sum over all
- * chunks), or NULL: dH alone. */
+ * chunks), or NULL: dH alone.  dH and dW must not overlap the inputs. */
 size_t kd_token_logp_backward_workspace_size(int64_t N, int64_t d, int64_t V, int64_t chunk, int dW_bf16);
 int kd_token_logp_backward(const void* H, const void* W, const void* labels, int labels_i64,
                            int64_t N, int64_t d, int64_t V, float T, int64_t chunk,

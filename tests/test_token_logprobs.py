@@ -117,7 +117,8 @@ def test_refusals_of_one_pass(kd):
     for bad in (dict(chunk=0), dict(lse=None), dict(dlogp=None), dict(dH=None), dict(dH=P + 8), dict(dW=P + 8),
                 dict(dent=P), dict(half=2), dict(half=1, acc=1), dict(dlogp=P + 2)):
         assert _bwd(kd, **bad) == _abi.KD_ERR_INVALID_ARG
-    for bad in (dict(d=60), dict(T=1e-7), dict(T=float("inf")), dict(N=1 << 31), dict(V=1 << 31)):
+    for bad in (dict(d=60), dict(T=1e-7), dict(T=float("inf")), dict(N=1 << 31), dict(V=1 << 31),
+                dict(N=(1 << 31) - 1000), dict(V=(1 << 31) - 1000)):
         assert _fwd(kd, **bad) == _abi.KD_ERR_UNSUPPORTED
         assert _bwd(kd, **bad) == _abi.KD_ERR_UNSUPPORTED
     assert _fwd(kd, nb=kd.kd_token_logp_forward_workspace_size(100, 64, 1000) - 1) == _abi.KD_ERR_WORKSPACE
