@@ -77,7 +77,7 @@ bool all_aligned16(std::initializer_list<const void*> ps) {
 
 void two_floats(double v, float* h, float* l) {
   *h = (float)v;
-  *l = (float)(v - (double)*h);
+  *l = std::isfinite(v) ? (float)(v - (double)*h) : 0.f;
 }
 
 int launched() { return cudaGetLastError() == cudaSuccess ? KD_OK : KD_ERR_CUDA; }
@@ -238,15 +238,16 @@ int kd_policy_loss(const float* logp, const float* old_logp, const float* ref_lo
   A.grad_loss = grad_loss;
   A.adv_per_seq = advantages_per_sequence;
   A.per_sequence = per_sequence;
-  two_floats(std::log1p(clip_high), &A.hi_h, &A.hi_l);
-  two_floats(std::log1p(-clip_low), &A.lo_h, &A.lo_l);
-  two_floats(std::log(dual_clip), &A.dual_h, &A.dual_l);
-  if (dual_clip == 0.0) {
-    A.dual_h = INFINITY;
-    A.dual_l = 0.f;
-  }
-  A.hi1 = (float)(1.0 + clip_high);
-  A.lo1 = (float)(1.0 - clip_low);
+  A.log_hi = std::log1p(clip_high);
+  A.log_lo = std::log1p(-clip_low);
+  A.log_dual = dual_clip == 0.0 ? INFINITY : std::log(dual_clip);
+  two_floats(A.log_hi, &A.hi_h, &A.hi_l);
+  two_floats(A.log_lo, &A.lo_h, &A.lo_l);
+  two_floats(A.log_dual, &A.dual_h, &A.dual_l);
+  A.hi1 = (float)(A.hi1_64 = 1.0 + clip_high);
+  A.lo1 = (float)(A.lo1_64 = 1.0 - clip_low);
+  A.dual_64 = dual_clip;
+  A.kl_coef_64 = kl_coef;
   A.dual_c = (float)dual_clip;
   A.kl_coef = (float)kl_coef;
   A.sums = reinterpret_cast<double*>(ws + L.off_sums);

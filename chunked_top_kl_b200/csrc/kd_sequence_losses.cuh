@@ -384,6 +384,7 @@ struct PolicyArgs {
   int adv_per_seq, per_sequence;
   float hi_h, hi_l, lo_h, lo_l, dual_h, dual_l;     // log borders in two floats each (no dual clip: infinity)
   float hi1, lo1, dual_c, kl_coef;                  // 1 + hi, 1 - lo, c
+  double log_hi, log_lo, log_dual, hi1_64, lo1_64, dual_64, kl_coef_64;      // the same
   double* sums;            // [S * splits] sum m; null: each team sums its own (whole) sequences' masks
   double* total;           // [kSumBlocks] the first launch's blocks' sums
   double* part;            // [blocks][3]
@@ -485,6 +486,35 @@ __device__ __forceinline__ void policy_token(const PolicyArgs& A, float lp, floa
   d = fmaf(A.kl_coef, dk, clip ? 0.f : -ra);
 }
 
+// The same in 64 bits.
+template <int KL>
+__device__ __forceinline__ void policy_token64(const PolicyArgs& A, float lp, float old, float ref, float a, double& loss,
+                                               double& kl, double& clipped, double& d) {
+  const double x = (double)lp - (double)old;
+  const bool under = x < A.log_lo;
+  const bool clip = a > 0.f ? x > A.log_hi : (a < 0.f && (under || x > A.log_dual));
+  const double border = a > 0.f ? A.hi1_64 : (under ? A.lo1_64 : A.dual_64);
+  const double ra = a == 0.f ? 0.0 : exp(x) * (double)a;
+  clipped = clip ? 1.0 : 0.0;
+  kl = 0.0;
+  double dk = 0.0;
+  if (KL != kNoKl) {
+    const double y = (double)lp - (double)ref;
+    if (KL == kK1) {
+      kl = y;
+      dk = 1.0;
+    } else if (KL == kK2) {
+      kl = 0.5 * y * y;
+      dk = y;
+    } else {
+      dk = -expm1(-y);
+      kl = y - dk;
+    }
+  }
+  loss = A.kl_coef_64 * kl - (clip ? border * (double)a : ra);
+  d = A.kl_coef_64 * dk - (clip ? 0.0 : ra);
+}
+
 // The blocks' partial scalars, joined in block order by one block.
 __device__ __forceinline__ void policy_join(const PolicyArgs& A, int blocks, double* red) {
   double v[3] = {0.0, 0.0, 0.0};
@@ -499,7 +529,7 @@ __device__ __forceinline__ void policy_join(const PolicyArgs& A, int blocks, dou
 }
 
 // The second phase, up to the block's partial scalars; sum_blocks: the first phase's blocks.
-template <int TEAM, bool VEC, int KL>
+template <int TEAM, bool VEC, int KL, bool WIDE>
 __device__ __forceinline__ void policy_losses(const PolicyArgs& A, int sum_blocks, double* red) {
   constexpr int kTeams = kThreads / TEAM;
   const int tid = threadIdx.x % TEAM;
@@ -543,16 +573,30 @@ __device__ __forceinline__ void policy_losses(const PolicyArgs& A, int sum_block
         load4<VEC>(A.old, t0, lo, hi, od);
         if (KL != kNoKl) load4<VEC>(A.ref, t0, lo, hi, rf);
         if (!A.adv_per_seq) load4<VEC>(A.adv, t0, lo, hi, a);
+        if constexpr (WIDE) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {         // a masked place may hold anything, NaN included
-          const bool on = m[j] != 0.f;
-          policy_token<KL>(A, on ? lp[j] : 0.f, on ? od[j] : 0.f, KL != kNoKl && on ? rf[j] : 0.f,
-                           on ? (A.adv_per_seq ? as : a[j]) : 0.f, l[j], k[j], c[j], d[j]);
-          d[j] = on ? wg * m[j] * d[j] : 0.f;
+          for (int j = 0; j < 4; ++j)
+            if (m[j] != 0.f) {                // a masked place may hold anything, NaN included
+              double l64, k64, c64, d64;
+              policy_token64<KL>(A, lp[j], od[j], KL != kNoKl ? rf[j] : 0.f, A.adv_per_seq ? as : a[j], l64, k64, c64, d64);
+              const double wm = w * (double)m[j];
+              sum_l += wm * l64;
+              sum_k += wm * k64;
+              sum_c += wm * c64;
+              d[j] = (float)((double)g * wm * d64);
+            }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {         // a masked place may hold anything, NaN included
+            const bool on = m[j] != 0.f;
+            policy_token<KL>(A, on ? lp[j] : 0.f, on ? od[j] : 0.f, KL != kNoKl && on ? rf[j] : 0.f,
+                             on ? (A.adv_per_seq ? as : a[j]) : 0.f, l[j], k[j], c[j], d[j]);
+            d[j] = on ? wg * m[j] * d[j] : 0.f;
+          }
+          sum_l += w * (double)fmaf(m[0], l[0], fmaf(m[1], l[1], fmaf(m[2], l[2], m[3] * l[3])));
+          sum_k += w * (double)fmaf(m[0], k[0], fmaf(m[1], k[1], fmaf(m[2], k[2], m[3] * k[3])));
+          sum_c += w * (double)fmaf(m[0], c[0], fmaf(m[1], c[1], fmaf(m[2], c[2], m[3] * c[3])));
         }
-        sum_l += w * (double)fmaf(m[0], l[0], fmaf(m[1], l[1], fmaf(m[2], l[2], m[3] * l[3])));
-        sum_k += w * (double)fmaf(m[0], k[0], fmaf(m[1], k[1], fmaf(m[2], k[2], m[3] * k[3])));
-        sum_c += w * (double)fmaf(m[0], c[0], fmaf(m[1], c[1], fmaf(m[2], c[2], m[3] * c[3])));
       }
       if (A.dlogp) store4<VEC>(A.dlogp, t0, lo, hi, d);
     }
@@ -582,7 +626,7 @@ template <int TEAM, bool VEC, int KL>
 __global__ void __launch_bounds__(kThreads, 5) policy_loss_kernel(const PolicyArgs A, int sum_blocks) {
   __shared__ double red[kThreads / 32];
   if (!A.sums) next_may_start();              // policy_finish_kernel
-  policy_losses<TEAM, VEC, KL>(A, sum_blocks, red);
+  policy_losses<TEAM, VEC, KL, false>(A, sum_blocks, red);
   if (A.sums && last_block(A.counter)) policy_join(A, gridDim.x, red);
 }
 
@@ -600,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, kResident) policy_one_kernel(const P
     policy_sums<TEAM, VEC>(A, red);
     cooperative_groups::this_grid().sync();
   }
-  policy_losses<TEAM, VEC, KL>(A, gridDim.x, red);
+  policy_losses<TEAM, VEC, KL, true>(A, gridDim.x, red);
   cooperative_groups::this_grid().sync();
   if (blockIdx.x == 0) policy_join(A, gridDim.x, red);
 }

@@ -81,7 +81,7 @@ typedef enum kd_status {
   KD_ERR_UNSUPPORTED = 2,  /* shape outside the supported set (d % 8, K > 512, ...) */
   KD_ERR_WORKSPACE = 3,    /* workspace_bytes smaller than kd_topk_kl_workspace_size */
   KD_ERR_CUDA = 4,         /* a CUDA runtime call or kernel launch failed */
-  KD_ERR_BAD_INDEX = 5,    /* (from kd_topk_kl_check) a teacher index was outside [0, V) */
+  KD_ERR_BAD_INDEX = 5,    /* (from kd_topk_kl_check) a teacher index was outside [0, V), or a label >= V */
   KD_ERR_TIMEOUT = 6       /* (from kd_topk_kl_check) a pipeline wait gave up; results invalid */
 } kd_status;
 
