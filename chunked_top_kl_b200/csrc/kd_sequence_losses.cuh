@@ -79,11 +79,12 @@ __device__ __forceinline__ void item_range(const Sequences& q, int64_t s, int k,
 }
 
 // Four tokens of an array from t0 (a multiple of 4): those of [lo, hi), zeros
-// for the others.
-template <bool VEC>
+// for the others.  ONCE: not read again, so not worth keeping in L2 (the mask is).
+template <bool VEC, bool ONCE = true>
 __device__ __forceinline__ void load4(const float* __restrict__ p, int t0, int lo, int hi, float (&v)[4]) {
   if (VEC && t0 >= lo && t0 + 4 <= hi) {
-    const float4 f = *reinterpret_cast<const float4*>(p + t0);
+    const float4* q = reinterpret_cast<const float4*>(p + t0);
+    const float4 f = ONCE ? __ldcs(q) : *q;
     v[0] = f.x;
     v[1] = f.y;
     v[2] = f.z;
@@ -97,7 +98,7 @@ __device__ __forceinline__ void load4(const float* __restrict__ p, int t0, int l
 template <bool VEC>
 __device__ __forceinline__ void store4(float* __restrict__ p, int t0, int lo, int hi, const float (&v)[4]) {
   if (VEC && t0 >= lo && t0 + 4 <= hi) {
-    *reinterpret_cast<float4*>(p + t0) = make_float4(v[0], v[1], v[2], v[3]);
+    __stcs(reinterpret_cast<float4*>(p + t0), make_float4(v[0], v[1], v[2], v[3]));
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -110,7 +111,7 @@ template <bool VEC>
 __device__ __forceinline__ void load_mask4(const float* __restrict__ mask, int t0, int lo, int hi,
                                            float (&m)[4]) {
   if (mask) {
-    load4<VEC>(mask, t0, lo, hi, m);
+    load4<VEC, false>(mask, t0, lo, hi, m);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) m[j] = (t0 + j >= lo && t0 + j < hi) ? 1.f : 0.f;
@@ -399,7 +400,7 @@ __device__ __forceinline__ double mask_sum(const float* __restrict__ mask, int l
   for (int t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM * kSumUnroll) {
     float m[kSumUnroll][4];
 #pragma unroll
-    for (int u = 0; u < kSumUnroll; ++u) load4<VEC>(mask, t0 + 4 * TEAM * u, lo, hi, m[u]);
+    for (int u = 0; u < kSumUnroll; ++u) load4<VEC, false>(mask, t0 + 4 * TEAM * u, lo, hi, m[u]);
 #pragma unroll
     for (int u = 0; u < kSumUnroll; ++u)
       n += ((double)m[u][0] + (double)m[u][1]) + ((double)m[u][2] + (double)m[u][3]);
