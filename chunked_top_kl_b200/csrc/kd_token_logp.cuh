@@ -502,26 +502,29 @@ logp_merge_kernel(const float* __restrict__ part_m, const float* __restrict__ pa
 
 // ---------------------------------------------------------------- a few tokens
 //
-// Up to kFewTokens tokens (a single token's score, a draft to verify): the
-// time is that of reading W once, 2 V d bytes, and the GEMM above, whose tiles
-// are 256 tokens high, reads it at 4.6 TB/s (250 us at V = 201,088, d = 2880,
-// one token).  Here each warp streams a contiguous range of W's rows straight
-// into registers, sixteen rows at a time, as the A operand of m16n8k16 products
-// with the tokens as columns: the tensor cores idle nearly all of the time, so
-// the plain warp-level product serves.  A thread's 16-byte load holds eight
-// consecutive k of a row where the product's layout wants two groups of two
-// times two; as every k counts alike, A and B take the same eight in the same
-// order.  H lies in shared memory in the order of the loads (few_smem bytes: a
-// d that does not fit goes to the GEMM); read through L1 it was pushed out by
-// the stream of W (206 us instead of 195 us for a token, 316 instead of 223 for
-// nine).  The running softmax state is as in EpiLogp, a thread holding two tokens
-// (per eight) over the rows it meets; warps, then blocks (through the partials,
-// one range per block) are joined.  195 us for a token at V = 201,088, d = 2880
-// (5.9 TB/s), 223 for sixteen, where the GEMM takes 228; seventeen and more took
-// 440 us here.
+// Up to eight tokens (a single token's score, a draft to verify): the time is
+// that of reading W once, 2 V d bytes, and the GEMM above, whose tiles are 256
+// tokens high, reads it at 4.6 TB/s (250 us at V = 201,088, d = 2880, one token).
+// Here each warp streams a contiguous range of W's rows straight into registers,
+// sixteen rows at a time, as the A operand of m16n8k16 products with the tokens
+// as columns: the tensor cores idle nearly all of the time, so the plain
+// warp-level product serves.  A thread's 16-byte load holds eight consecutive k
+// of a row where the product's layout wants two groups of two times two; as every
+// k counts alike, A and B take the same eight in the same order.  H lies in shared
+// memory in the order of the loads (few_smem bytes: a d that does not fit goes to
+// the GEMM); read through L1 it was pushed out by the stream of W (206 us instead
+// of 195 us for a token).  The running softmax state is as in EpiLogp, a thread
+// holding two tokens (per eight) over the rows it meets; warps, then blocks
+// (through the partials, one range per block) are joined.
+//
+// Measured against the GEMM's 128-row tiles (us): V = 201,088, d = 2880, up to
+// eight tokens 195, nine to sixteen 223 against 202; V = 32,000, d = 2048, 37, and
+// 45 against 50; V = 8,000, d = 512, 15 against 20.  So nine to sixteen tokens come
+// here where W is small (kFewWideBytes) and launches are a part of the time.
 //
 // Every kFewBatch k blocks the products start from zero and are added up in
 // fp32 with rounding: sums so short need no accumulation_gain.
+constexpr int64_t kFewWideBytes = 200 << 20;
 constexpr int kFewTokens = 16;
 constexpr int kFewWarps = 8, kFewThreads = 32 * kFewWarps;
 constexpr int kFewBatch = 4;                  // k blocks of 32 whose loads are in flight together

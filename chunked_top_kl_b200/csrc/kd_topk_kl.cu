@@ -169,7 +169,7 @@ struct DevInfo {
   int sms = 0;
   int pair_groups = 0;          // co-resident CTA pairs of the GEMM kernel
   int64_t l2_bytes = 0;
-  bool attr_set[16] = {};     // by launch_gemm's slot
+  bool attr_set[20] = {};     // by launch_gemm's slot
 };
 DevInfo g_dev[kMaxDevices];
 
@@ -917,10 +917,18 @@ int logp_common(const void* H, const void* W, const void* labels, int labels_i64
   return KD_OK;
 }
 
+// Up to 128 tokens fill half of a CTA pair's 256-row tile: the forward product
+// then runs 128-row tiles of one CTA each, half the products (which W's bytes no
+// longer hide) for the same bytes: 64 tokens at V = 201,088, d = 2880 250-260 us
+// in pairs, 209 us (5.5 TB/s) in single CTAs; V = 32,000, d = 2048 61 and 49 us.
+constexpr int64_t kSingleRows = 128;
+constexpr int kSingleMaxSplits = 160;       // column ranges of the one band: a range for every SM
+
 template <bool ENT>
 int logp_forward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, float T, float* logp, float* lse,
                  float* ent, const LogpLayout& L, void* ws, int dev, cudaStream_t s, LabelPrep lp) {
-  const int groups = resident_groups(dev);
+  const bool single = N <= kSingleRows;      // 128-row tiles of one CTA each
+  const int groups = single ? device_sms(dev) : resident_groups(dev);
   const int64_t n_tiles = ceil_div(V, BN), most = ceil_div(N, GeoP::TILE_M) * n_tiles;
   LiveRows* live = at<LiveRows>(ws, L.off_live);
   unsigned int* wave = at<unsigned int>(ws, L.off_wave);
@@ -929,7 +937,7 @@ int logp_forward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, 
   lp.ent = ent;
   lp.n_tiles = (int)n_tiles;
   lp.groups = (int)(most < groups ? most : groups);
-  lp.max_splits = kLogpMaxSplits;
+  lp.max_splits = single ? kSingleMaxSplits : kLogpMaxSplits;
   lp.part_slots = L.slots;
   lp.band_bytes = GeoP::TILE_M * d * 2;
   lp.l2_bytes = device_l2_bytes(dev);
@@ -946,7 +954,8 @@ int logp_forward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, 
     return KD_ERR_CUDA;
 
   CUtensorMap tmH, tmW;
-  if (!make_map(&tmH, hc, d, N > kPadRows ? N : kPadRows, d, BK, BM) || !make_map(&tmW, W, d, V, d, BK, GeoP::B_ROWS)) return KD_ERR_CUDA;
+  if (!make_map(&tmH, hc, d, N > kPadRows ? N : kPadRows, d, BK, BM) || !make_map(&tmW, W, d, V, d, BK, single ? Geo<false>::B_ROWS : GeoP::B_ROWS))
+    return KD_ERR_CUDA;
   ProbArgs a{};
   a.raster.n_tiles = (int)n_tiles;
   a.num_kb = (int)ceil_div(d, BK);
@@ -960,9 +969,20 @@ int logp_forward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, 
   ep.part_s = part + L.slots;
   ep.part_g = part + 2 * L.slots;
   ep.part_t = part + 3 * L.slots;
-  if (launch_one<ProbLogp<ENT>>(ENT ? 5 : 4, dev, lp.groups, tmH, tmW, tmH, a, lp.status, ep, s,
-                                DynRows{&live->count, 0, (int)N, &live->raster}, wave, true) != cudaSuccess)
-    return KD_ERR_CUDA;
+  const DynRows dyn{&live->count, 0, (int)N, &live->raster};
+  cudaError_t e;
+  if (single) {
+    GemmArgs ga{};
+    ga.prob[0] = a;
+    ga.status = lp.status;
+    ga.dyn = dyn;
+    EpiNone::Params none{};
+    e = launch_gemm<ProbLogp<ENT>, NoProb, false>(ENT ? 16 : 15, dev, lp.groups, tmH, tmW, tmH, tmH, tmW, tmH, ga, ep, none,
+                                                  s, true);
+  } else {
+    e = launch_one<ProbLogp<ENT>>(ENT ? 5 : 4, dev, lp.groups, tmH, tmW, tmH, a, lp.status, ep, s, dyn, wave, true);
+  }
+  if (e != cudaSuccess) return KD_ERR_CUDA;
   return launch_next(logp_merge_kernel<ENT, 32, 8>, (unsigned)ceil_div(N, 32), 256u, s, ep.part_m, ep.part_s, ep.part_t,
                      ep.part_g, live, lp.rowmap, zlab, ep.zl2, kLog2e / T, logp, lse, ent, lp.status) == cudaSuccess
              ? KD_OK
@@ -1184,7 +1204,7 @@ int kd_token_logp_forward(const void* H, const void* W, const void* labels, int 
                                                                                                      : KD_ERR_CUDA;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KD_ERR_CUDA;
-  if (N <= kFewTokens && few_smem(N, d) <= kFewSmem)
+  if ((N <= 8 || (N <= kFewTokens && 2 * V * d <= kFewWideBytes)) && few_smem(N, d) <= kFewSmem)
     return entropy ? logp_forward_few<true>(H, W, labels, labels_i64, N, d, V, T, logp, lse, entropy, L, workspace, dev, s)
                    : logp_forward_few<false>(H, W, labels, labels_i64, N, d, V, T, logp, lse, nullptr, L, workspace, dev, s);
   const LabelPrep lp = label_prep(labels, labels_i64, N, V, L, workspace);

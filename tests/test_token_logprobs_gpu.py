@@ -132,11 +132,11 @@ def test_both_passes(kd, N, d, V, ignored, i64, T, ent):
     _check_backward(dH4, None, H, W, y, g, h if ent else None, T)
 
 
-@pytest.mark.parametrize("N", [1, 7, 8, 9, 16, 17, 31, 32, 33])
+@pytest.mark.parametrize("N", [1, 7, 8, 9, 16, 17, 33, 64, 127, 128, 129])
 @pytest.mark.parametrize("d,V", [(8, 3), (40, 129), (1000, 5003), (2880, 40000)])
 @pytest.mark.parametrize("ignored", ["none", "some"])
 def test_a_few_tokens(kd, N, d, V, ignored):
-    """Both sides of the border between the streaming pass and the GEMM, with and without entropies, and a token
+    """Both sides of the borders between the streaming pass and the GEMM, with and without entropies, and a token
     that the labels leave out in any place."""
     H, W, y, _, _ = _inputs(N, d, V, N + d, ignored)
     if ignored == "some":
