@@ -38,6 +38,8 @@ def _check_workspace(ws, dev) -> None:
 def _grad_scalar(grad_loss, dev):
     if grad_loss is None:
         return None
+    if grad_loss.dim() == 0 and grad_loss.dtype == torch.float32 and grad_loss.device == dev:
+        return grad_loss
     if grad_loss.numel() != 1:
         raise ValueError("kd_topk_kl: grad_loss must hold one value")
     return grad_loss.reshape(()).to(device=dev, dtype=torch.float32).contiguous()

@@ -97,19 +97,27 @@ def token_logprobs_backward(H, W, labels, lse, dlogp, T: float = 1.0, chunk: int
         raise TypeError(f"{where}: dW must be float32 or bfloat16, got {dW_dtype}")
     if accumulate_dW and (dW is None or dW_dtype != torch.float32):
         raise ValueError(f"{where}: accumulate_dW needs a float32 dW to add to")
-    half = int(dW_dtype == torch.bfloat16)
     if dW is not None:
         _check_buffer(dW, "dW", (V, d), dW_dtype, dev)
-    elif dW_dtype is not None:
+    if workspace is not None:
+        _check_workspace(workspace, dev)
+    return _backward(H, W, labels, lse, dlogp, T, chunk, entropy, dentropy, dW, accumulate_dW, dW_dtype, workspace)
+
+
+def _backward(H, W, labels, lse, dlogp, T, chunk, entropy, dentropy, dW, accumulate_dW, dW_dtype, workspace):
+    """token_logprobs_backward on checked arguments."""
+    N, d = H.shape
+    V = W.shape[0]
+    dev = H.device
+    half = int(dW_dtype == torch.bfloat16)
+    if dW is None and dW_dtype is not None:
         dW = torch.empty((V, d), dtype=dW_dtype, device=dev)
-    dH = torch.empty((N, d), dtype=torch.bfloat16, device=dev)
+    dH = torch.empty_like(H)
     if workspace is None:
         n = _abi.kd_token_logp_backward_workspace_size(N, d, V, int(chunk), half)
         if n == 0:
-            raise ValueError(f"{where}: unsupported sizes")
+            raise ValueError("token_logprobs_backward: unsupported sizes")
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    else:
-        _check_workspace(workspace, dev)
     with _on(dev):
         st = _abi.kd_token_logp_backward(_ptr(H), _ptr(W), _ptr(labels), int(labels.dtype == torch.int64), N, d, V,
                                          float(T), int(chunk), _ptr(lse), _ptr(entropy), _ptr(dlogp), _ptr(dentropy),
@@ -139,8 +147,8 @@ class TokenLogprobsFunction(torch.autograd.Function):
             ent = None
         else:
             dent = dent.contiguous()
-        dH, dW = token_logprobs_backward(H, W, labels, lse, dlogp, ctx.T, ctx.chunk, ent, dent,
-                                         dW_dtype=W.dtype if ctx.needs_input_grad[1] else None)
+        dH, dW = _backward(H, W, labels, lse, dlogp, ctx.T, ctx.chunk, ent, dent, None, False,
+                           W.dtype if ctx.needs_input_grad[1] else None, None)
         return dH, dW, None, None, None, None
 
 
