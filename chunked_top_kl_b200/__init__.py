@@ -18,7 +18,7 @@ from .api import (KDTopKKLFunction, alloc_workspace, backward, backward_launches
                   forward_backward, forward_backward_launches, kd_topk_kl_loss, teacher_topk, workspace_bytes)
 from .sequence_losses import (PolicyLossFunction, PreferenceLossFunction, policy_loss, policy_loss_forward_backward,
                               preference_loss, preference_loss_forward_backward)
-from .token_logprobs import (TokenLogprobsFunction, token_logprobs, token_logprobs_backward, token_logprobs_forward)
+from .logprobs import (TokenLogprobsFunction, token_logprobs, token_logprobs_backward, token_logprobs_forward)
 
 __all__ = [
     "EXPORTS", "KDError", "kd_policy_loss", "kd_preference_loss", "kd_scale_gradient",

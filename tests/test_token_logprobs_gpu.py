@@ -14,12 +14,14 @@ Tolerances, elementwise, with u = 2^-24 and half a bf16 step b = 2^-8:
   every term.
 """
 
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 import oracle
-from oracle.token_logprobs import _logq
+from oracle.logprobs import _logq
 
 pytestmark = pytest.mark.gpu
 
@@ -437,3 +439,31 @@ def test_binding_refuses(kd):
             call()
     with pytest.raises(kd.KDError):
         kd.token_logprobs_forward(H, W, y, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+
+
+def test_calls_are_made_on_the_inputs_device_and_stream(kd, monkeypatch):
+    """Each library call is made with the inputs' device current and on its current stream (the losses' calls too)."""
+    seen = []
+
+    def spy(module, name):
+        real = getattr(module, name)
+
+        def call(dev):
+            seen.append((name, dev))
+            return real(dev)
+        monkeypatch.setattr(module, name, call)
+    for m in ("logprobs", "sequence_losses"):
+        spy(sys.modules["chunked_top_kl_b200." + m], "_on")
+        spy(sys.modules["chunked_top_kl_b200." + m], "_stream")
+    H, W, y, g, _ = (t.cuda() for t in _inputs(40, 16, 50, 3, "some"))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        lse = kd.token_logprobs_forward(H, W, y)[1]
+        kd.token_logprobs_backward(H, W, y, lse, g)
+        x = torch.zeros(2, 20, device="cuda", requires_grad=True)
+        kd.preference_loss(x)[0].backward()
+        kd.policy_loss(x, x.detach(), x.detach())[0].backward()
+    s.synchronize()
+    dev = H.device
+    assert seen == [("_on", dev), ("_stream", dev)] * 6
