@@ -140,6 +140,51 @@ __device__ __forceinline__ double team_sum(double v, double* red) {
   return v;
 }
 
+// Calls body(team, item, lo, hi, thread in the team) for the block's items; every
+// thread of a team calls together.  Among short sequences one that is long is
+// left to the whole block: a warp would still be at it when all others are done
+// (32,768 tokens among 2,000 sequences of 150: policy loss 84 us, by warps alone
+// 480; 200,000 sequences of 100 tokens pay 3% for the question).
+constexpr int kWarpItemTokens = 2048;
+
+template <int T>
+struct Team {
+  static constexpr int threads = T;
+};
+
+template <int TEAM, class Body>
+__device__ __forceinline__ void for_items(const Sequences& q, Body&& body) {
+  const int64_t items = q.S * q.splits;
+  auto range = [&](int64_t it, int& lo, int& hi) {
+    const int64_t s = it / q.splits;
+    item_range(q, s, (int)(it - s * q.splits), lo, hi);
+  };
+  if constexpr (TEAM == kThreads) {
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+      int lo, hi;
+      range(it, lo, hi);
+      body(Team<kThreads>{}, it, lo, hi, (int)threadIdx.x);
+    }
+  } else {
+    constexpr int kTeams = kThreads / TEAM;
+    const int64_t first = (int64_t)blockIdx.x * kTeams, step = (int64_t)gridDim.x * kTeams;
+    bool left = false;
+    for (int64_t it = first + threadIdx.x / TEAM; it < items; it += step) {
+      int lo, hi;
+      range(it, lo, hi);
+      if (hi - lo <= kWarpItemTokens) body(Team<TEAM>{}, it, lo, hi, (int)(threadIdx.x % TEAM));
+      else left = true;
+    }
+    if (__syncthreads_or(left))               // after the short ones: no warp waits for another on the way
+      for (int64_t base = first; base < items; base += step)
+        for (int64_t it = base; it < base + kTeams && it < items; ++it) {
+          int lo, hi;
+          range(it, lo, hi);
+          if (hi - lo > kWarpItemTokens) body(Team<kThreads>{}, it, lo, hi, (int)threadIdx.x);
+        }
+  }
+}
+
 // Sum of n values, by the lanes of one warp in a fixed order.
 __device__ __forceinline__ double warp_sum_array(const double* p, int64_t n, int stride) {
   double v = 0.0;
@@ -197,19 +242,14 @@ struct PrefArgs {
 
 template <int TEAM, bool VEC>
 __device__ __forceinline__ void pref_sums(const PrefArgs& A, double* red) {
-  constexpr int kTeams = kThreads / TEAM;
-  const int tid = threadIdx.x % TEAM;
-  const int64_t items = A.q.S * A.q.splits;
-  for (int64_t it = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; it < items; it += (int64_t)gridDim.x * kTeams) {
-    const int64_t s = it / A.q.splits;
-    int lo, hi;
-    item_range(A.q, s, (int)(it - s * A.q.splits), lo, hi);
+  for_items<TEAM>(A.q, [&](auto team, int64_t it, int lo, int hi, int tid) {
+    constexpr int T = decltype(team)::threads;
     double r = 0.0, n = 0.0;
-    for (int t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM * kSumUnroll) {
+    for (int t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * T * kSumUnroll) {
       float m[kSumUnroll][4], lp[kSumUnroll][4], rf[kSumUnroll][4];
 #pragma unroll
       for (int u = 0; u < kSumUnroll; ++u) {
-        const int t = t0 + 4 * TEAM * u;
+        const int t = t0 + 4 * T * u;
         load_mask4<VEC>(A.mask, t, lo, hi, m[u]);
         load4<VEC>(A.logp, t, lo, hi, lp[u]);
         if (A.ref) load4<VEC>(A.ref, t, lo, hi, rf[u]);
@@ -223,13 +263,13 @@ __device__ __forceinline__ void pref_sums(const PrefArgs& A, double* red) {
             n += (double)m[u][j];
           }
     }
-    r = team_sum<TEAM>(r, red);
-    n = team_sum<TEAM>(n, red);
+    r = team_sum<T>(r, red);
+    n = team_sum<T>(n, red);
     if (tid == 0) {
       A.sums[2 * it] = r;
       A.sums[2 * it + 1] = n;
     }
-  }
+  });
 }
 
 // Sequence s's log ratio and the factor of its tokens' weights (a whole warp calls).
@@ -253,21 +293,18 @@ __device__ __forceinline__ double softplus64(double v) { return (v > 0.0 ? v : 0
 template <int TEAM, bool VEC>
 __device__ __forceinline__ void pref_losses(const PrefArgs& A, double* red) {
   __shared__ float s_coef;
-  constexpr int kTeams = kThreads / TEAM;
-  const int tid = threadIdx.x % TEAM;
-  const int64_t items = A.q.S * A.q.splits, P = A.q.S / 2;
+  const int64_t P = A.q.S / 2;
   const double g = A.grad_loss ? (double)*A.grad_loss : 1.0;
   double mine = 0.0;                          // pair losses of this thread's teams
-  for (int64_t it = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; it < items; it += (int64_t)gridDim.x * kTeams) {
+  for_items<TEAM>(A.q, [&](auto team, int64_t it, int lo, int hi, int tid) {
+    constexpr int T = decltype(team)::threads;
     const int64_t s = it / A.q.splits;
     const int k = (int)(it - s * A.q.splits);
-    int lo, hi;
-    item_range(A.q, s, k, lo, hi);
     float m[kSumUnroll][4];                   // the first groups' masks arrive while the coefficient is worked out
     if (A.dlogp)
 #pragma unroll
       for (int u = 0; u < kSumUnroll; ++u)
-        load_mask4<VEC>(A.mask, (((lo >> 2) + tid) << 2) + 4 * TEAM * u, lo, hi, m[u]);
+        load_mask4<VEC>(A.mask, (((lo >> 2) + tid) << 2) + 4 * T * u, lo, hi, m[u]);
     float coef = 0.f;
     wait_previous();                          // for the sums
     if (tid < 32) {
@@ -294,14 +331,14 @@ __device__ __forceinline__ void pref_losses(const PrefArgs& A, double* red) {
         }
       }
     }
-    if (!A.dlogp) continue;
-    if constexpr (TEAM > 32) {
+    if (!A.dlogp) return;
+    if constexpr (T > 32) {
       if (threadIdx.x == 0) s_coef = coef;
       __syncthreads();
       coef = s_coef;
       __syncthreads();
     }
-    for (int t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM * kSumUnroll) {
+    for (int t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * T * kSumUnroll) {
       float d[kSumUnroll][4];
 #pragma unroll
       for (int u = 0; u < kSumUnroll; ++u)
@@ -309,14 +346,14 @@ __device__ __forceinline__ void pref_losses(const PrefArgs& A, double* red) {
         for (int j = 0; j < 4; ++j) d[u][j] = m[u][j] != 0.f ? coef * m[u][j] : 0.f;
 #pragma unroll
       for (int u = 0; u < kSumUnroll; ++u)
-        load_mask4<VEC>(A.mask, t0 + 4 * TEAM * (u + kSumUnroll), lo, hi, m[u]);
+        load_mask4<VEC>(A.mask, t0 + 4 * T * (u + kSumUnroll), lo, hi, m[u]);
 #pragma unroll
       for (int u = 0; u < kSumUnroll; ++u) {
-        const int t = t0 + 4 * TEAM * u;
+        const int t = t0 + 4 * T * u;
         if (t < hi) store4<VEC>(A.dlogp, t, lo, hi, d[u]);
       }
     }
-  }
+  });
   wait_previous();                            // a block without an item, too: the counter is the first launch's
   if (A.dlogp) zero_outside(A.q, A.dlogp);
   mine = team_sum<kThreads>(mine, red);
@@ -410,20 +447,15 @@ __device__ __forceinline__ double mask_sum(const float* __restrict__ mask, int l
 
 template <int TEAM, bool VEC>
 __device__ __forceinline__ void policy_sums(const PolicyArgs& A, double* red) {
-  constexpr int kTeams = kThreads / TEAM;
-  const int tid = threadIdx.x % TEAM;
-  const int64_t items = A.q.S * A.q.splits;
   double all = 0.0;
-  for (int64_t it = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; it < items; it += (int64_t)gridDim.x * kTeams) {
-    const int64_t s = it / A.q.splits;
-    int lo, hi;
-    item_range(A.q, s, (int)(it - s * A.q.splits), lo, hi);
-    const double n = A.mask ? team_sum<TEAM>(mask_sum<TEAM, VEC>(A.mask, lo, hi, tid), red) : (double)(hi - lo);
+  for_items<TEAM>(A.q, [&](auto team, int64_t it, int lo, int hi, int tid) {
+    constexpr int T = decltype(team)::threads;
+    const double n = A.mask ? team_sum<T>(mask_sum<T, VEC>(A.mask, lo, hi, tid), red) : (double)(hi - lo);
     if (tid == 0) {
       A.sums[it] = n;
       all += n;
     }
-  }
+  });
   all = team_sum<kThreads>(all, red);
   if (threadIdx.x == 0) A.total[blockIdx.x] = all;
 }
@@ -532,9 +564,6 @@ __device__ __forceinline__ void policy_join(const PolicyArgs& A, int blocks, dou
 // The second phase, up to the block's partial scalars; sum_blocks: the first phase's blocks.
 template <int TEAM, bool VEC, int KL, bool WIDE>
 __device__ __forceinline__ void policy_losses(const PolicyArgs& A, int sum_blocks, double* red) {
-  constexpr int kTeams = kThreads / TEAM;
-  const int tid = threadIdx.x % TEAM;
-  const int64_t items = A.q.S * A.q.splits;
   const float g = A.grad_loss ? *A.grad_loss : 1.f;
   double inv_total = 0.0;
   if (A.sums) wait_previous();
@@ -545,31 +574,29 @@ __device__ __forceinline__ void policy_losses(const PolicyArgs& A, int sum_block
     inv_total = t != 0.0 ? 1.0 / t : 0.0;
   }
   double sum_l = 0.0, sum_k = 0.0, sum_c = 0.0;
-  for (int64_t it = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; it < items; it += (int64_t)gridDim.x * kTeams) {
+  for_items<TEAM>(A.q, [&](auto team, int64_t it, int lo, int hi, int tid) {
+    constexpr int T = decltype(team)::threads;
     const int64_t s = it / A.q.splits;
-    int lo, hi;
-    item_range(A.q, s, (int)(it - s * A.q.splits), lo, hi);
     double w = inv_total;
     if (A.per_sequence) {
       double n = 0.0;
       if (A.sums) {
         n = warp_sum_array(A.sums + s * A.q.splits, A.q.splits, 1);             // every warp of the team
       } else if (A.mask) {                    // the mask's second reading, below, finds it in L1
-        n = team_sum<TEAM>(mask_sum<TEAM, VEC>(A.mask, lo, hi, tid), red);
+        n = team_sum<T>(mask_sum<T, VEC>(A.mask, lo, hi, tid), red);
       } else {
         n = (double)(hi - lo);
       }
       w = n != 0.0 ? 1.0 / (n * (double)A.q.S) : 0.0;
     }
-    const float wg = (float)w * g;
     const float as = A.adv_per_seq ? A.adv[s] : 0.f;
     float next[4];                            // the next group's mask, loaded a group ahead
     load_mask4<VEC>(A.mask, ((lo >> 2) + tid) << 2, lo, hi, next);
-    for (int t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * TEAM) {
+    for (int t0 = ((lo >> 2) + tid) << 2; t0 < hi; t0 += 4 * T) {
       float m[4] = {next[0], next[1], next[2], next[3]}, d[4] = {0.f, 0.f, 0.f, 0.f};
-      load_mask4<VEC>(A.mask, t0 + 4 * TEAM, lo, hi, next);
+      load_mask4<VEC>(A.mask, t0 + 4 * T, lo, hi, next);
       if (w != 0.0 && (m[0] != 0.f || m[1] != 0.f || m[2] != 0.f || m[3] != 0.f)) {     // padding costs its mask alone
-        float lp[4], od[4], rf[4], a[4], l[4], k[4], c[4];
+        float lp[4], od[4], rf[4], a[4];
         load4<VEC>(A.logp, t0, lo, hi, lp);
         load4<VEC>(A.old, t0, lo, hi, od);
         if (KL != kNoKl) load4<VEC>(A.ref, t0, lo, hi, rf);
@@ -587,6 +614,8 @@ __device__ __forceinline__ void policy_losses(const PolicyArgs& A, int sum_block
               d[j] = (float)((double)g * wm * d64);
             }
         } else {
+          const float wg = (float)w * g;
+          float l[4], k[4], c[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {         // a masked place may hold anything, NaN included
             const bool on = m[j] != 0.f;
@@ -601,7 +630,7 @@ __device__ __forceinline__ void policy_losses(const PolicyArgs& A, int sum_block
       }
       if (A.dlogp) store4<VEC>(A.dlogp, t0, lo, hi, d);
     }
-  }
+  });
   if (A.dlogp) zero_outside(A.q, A.dlogp);
   sum_l = team_sum<kThreads>(sum_l, red);
   sum_k = team_sum<kThreads>(sum_k, red);
@@ -621,8 +650,9 @@ __global__ void __launch_bounds__(kThreads, 8) policy_sums_kernel(const PolicyAr
   policy_sums<TEAM, VEC>(A, red);
 }
 
-// Five blocks an SM, 48 registers a thread and some spills: 75.5 us against 79.4
-// with four, for 22 million padded tokens (7.2 million of them unmasked).
+// Five blocks an SM, 48 registers a thread and some spills: 69.8 us against 77.0
+// with four, for 22 million padded tokens (7.2 million of them unmasked).  Six take
+// 68.9 there, but 253 against 248 for 20 million tokens in sequences of 100.
 template <int TEAM, bool VEC, int KL>
 __global__ void __launch_bounds__(kThreads, 5) policy_loss_kernel(const PolicyArgs A, int sum_blocks) {
   __shared__ double red[kThreads / 32];

@@ -46,6 +46,9 @@ LAYOUTS = {
     "block_edges": ([1023, 1024, 1025, 4097], 1, 3),
     "long_pair": ([70001, 65537], 5, 1),
     "one_long_among_short": ([50000, 300, 200, 250, 1, 0, 257, 400], 0, 0),
+    "long_among_many_short": ([(11 * i) % 160 + (2047 + i // 40 if i % 40 == 7 else 0) for i in range(601)]
+                              + [9001], 3, 1),
+    "long_among_many_short_two_launches": ([90 + i % 50 + (3001 if i % 1500 == 1 else 0) for i in range(9500)], 1, 2),
 }
 
 
