@@ -9,7 +9,8 @@ been built; there is no fallback path.
 
 from ._abi import (EXPORTS, KDError, kd_policy_loss, kd_preference_loss, kd_scale_gradient,
                    kd_sequence_loss_workspace_size, kd_status_string, kd_teacher_topk, kd_teacher_topk_workspace_size,
-                   kd_token_logp_backward, kd_token_logp_backward_workspace_size, kd_token_logp_forward,
+                   kd_token_logp_backward, kd_token_logp_backward_ex, kd_token_logp_backward_workspace_size,
+                   kd_token_logp_forward, kd_token_logp_forward_ex,
                    kd_token_logp_forward_workspace_size, kd_topk_kl_backward, kd_topk_kl_backward_ex, kd_topk_kl_backward_profiled, kd_topk_kl_check,
                    kd_topk_kl_forward, kd_topk_kl_forward_backward, kd_topk_kl_forward_backward_ex,
                    kd_topk_kl_forward_ex, kd_topk_kl_forward_noalloc, kd_topk_kl_workspace_size, load,
@@ -23,7 +24,8 @@ from .logprobs import (TokenLogprobsFunction, token_logprobs, token_logprobs_bac
 __all__ = [
     "EXPORTS", "KDError", "kd_policy_loss", "kd_preference_loss", "kd_scale_gradient",
     "kd_sequence_loss_workspace_size", "kd_status_string", "kd_teacher_topk", "kd_teacher_topk_workspace_size",
-    "kd_token_logp_backward", "kd_token_logp_backward_workspace_size", "kd_token_logp_forward",
+    "kd_token_logp_backward", "kd_token_logp_backward_ex", "kd_token_logp_backward_workspace_size",
+    "kd_token_logp_forward", "kd_token_logp_forward_ex",
     "kd_token_logp_forward_workspace_size", "kd_topk_kl_backward", "kd_topk_kl_backward_ex", "kd_topk_kl_backward_profiled", "kd_topk_kl_check",
     "kd_topk_kl_forward", "kd_topk_kl_forward_backward", "kd_topk_kl_forward_backward_ex", "kd_topk_kl_forward_ex",
     "kd_topk_kl_forward_noalloc", "kd_topk_kl_workspace_size", "kd_selftest_wait_timeout", "load", "make_options",

@@ -36,8 +36,10 @@ EXPORTS = (
     "kd_teacher_topk",
     "kd_token_logp_forward_workspace_size",
     "kd_token_logp_forward",
+    "kd_token_logp_forward_ex",
     "kd_token_logp_backward_workspace_size",
     "kd_token_logp_backward",
+    "kd_token_logp_backward_ex",
     "kd_sequence_loss_workspace_size",
     "kd_preference_loss",
     "kd_policy_loss",
@@ -110,11 +112,16 @@ def load() -> ctypes.CDLL:
         lib.kd_token_logp_forward_workspace_size.restype = sz
         lib.kd_token_logp_forward.argtypes = [p, p, p, i32, i64, i64, i64, f32, p, p, p, p, sz, p]
         lib.kd_token_logp_forward.restype = i32
+        lib.kd_token_logp_forward_ex.argtypes = [p, p, p, i32, i64, i64, i64, f32, p, p, p, p, p, sz, p]
+        lib.kd_token_logp_forward_ex.restype = i32
         lib.kd_token_logp_backward_workspace_size.argtypes = [i64, i64, i64, i64, i32]
         lib.kd_token_logp_backward_workspace_size.restype = sz
         lib.kd_token_logp_backward.argtypes = [p, p, p, i32, i64, i64, i64, f32, i64, p, p, p, p, p, p, i32, i32,
                                                p, sz, p]
         lib.kd_token_logp_backward.restype = i32
+        lib.kd_token_logp_backward_ex.argtypes = [p, p, p, i32, i64, i64, i64, f32, i64, p, p, p, p, p, p, p, i32, i32,
+                                                  p, sz, p]
+        lib.kd_token_logp_backward_ex.restype = i32
         f64 = ctypes.c_double
         lib.kd_sequence_loss_workspace_size.argtypes = [i64]
         lib.kd_sequence_loss_workspace_size.restype = sz
@@ -253,6 +260,12 @@ def kd_token_logp_forward(H, W, labels, labels_i64, N, d, V, T, logp, lse, entro
                                             workspace_bytes, stream))
 
 
+def kd_token_logp_forward_ex(H, W, labels, labels_i64, N, d, V, T, logp, lse, entropy, logp_kept, workspace,
+                             workspace_bytes, stream) -> int:
+    return int(load().kd_token_logp_forward_ex(H, W, labels, labels_i64, N, d, V, T, logp, lse, entropy, logp_kept,
+                                               workspace, workspace_bytes, stream))
+
+
 def kd_token_logp_backward_workspace_size(N: int, d: int, V: int, chunk: int, dW_bf16: int) -> int:
     return int(load().kd_token_logp_backward_workspace_size(N, d, V, chunk, dW_bf16))
 
@@ -262,6 +275,13 @@ def kd_token_logp_backward(H, W, labels, labels_i64, N, d, V, T, chunk, lse, ent
     return int(load().kd_token_logp_backward(H, W, labels, labels_i64, N, d, V, T, chunk, lse, entropy, dlogp,
                                              dentropy, dH, dW, dW_bf16, accumulate_dW, workspace, workspace_bytes,
                                              stream))
+
+
+def kd_token_logp_backward_ex(H, W, labels, labels_i64, N, d, V, T, chunk, lse, entropy, logp, dlogp, dentropy, dH, dW,
+                              dW_bf16, accumulate_dW, workspace, workspace_bytes, stream) -> int:
+    return int(load().kd_token_logp_backward_ex(H, W, labels, labels_i64, N, d, V, T, chunk, lse, entropy, logp, dlogp,
+                                                dentropy, dH, dW, dW_bf16, accumulate_dW, workspace, workspace_bytes,
+                                                stream))
 
 
 def kd_sequence_loss_workspace_size(S: int) -> int:

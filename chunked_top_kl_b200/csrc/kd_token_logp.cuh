@@ -186,6 +186,7 @@ struct RowCoef {
 // The backward pass's share of gather_live_kernel.
 struct RowScales {
   const float *lse, *ent, *dlogp, *dent;   // ent and dent null without an entropy gradient
+  const float* logp;        // the forward pass's, or null
   float zs;                 // 1 / T
   RowCoef* coef;            // [C]
   float* scale;             // [C]
@@ -200,19 +201,27 @@ struct RowScales {
 // a scale that makes the label's entry exactly 1 or -1: it is the largest, and
 // its rounding error would be a common factor of the token's whole dH row.  dH
 // is multiplied by the scale in fp32, and dW = dZ^T H takes it with H, whose
-// elements round independently.  With pl = p at the label, from the exact logit:
+// elements round independently.  With pl = p at the label:
 //   without an entropy gradient  scale = -g (1 - pl) / T, dZ / scale = p / (1 - pl)
 //   (1 - pl folded into the exponent), -1 at the label;
 //   with one, a = -(g + h ent) / T, b = -h ln 2 / T, the label's entry
 //   L = (g (1 - pl) - h pl (log pl + ent)) / T is the scale unless it is small
 //   beside |g| + |h| (then that is, and L / scale is rounded as the others are).
+// log pl is z_y / T - lse from the exact logit, about 1e-6 off where lse is 20
+// (its rounding): below 2^-14 of 1 - pl = 1/16, but all of a 1 - pl of 1e-6.  So
+// where 1 - pl is below 1/16 the forward pass's log pl is taken, which is exact
+// to some 1e-5 of itself; without one (`logp` null) the 1e-6 stay.
 __device__ __forceinline__ RowCoef row_coef(const RowScales& B, int n, float zy, float& scale) {
   RowCoef c;
-  const float logp = fmaf(zy, B.zs, -B.lse[n]), g = B.dlogp[n] * B.zs;
-  const float om = -expm1f(logp);
+  const float g = B.dlogp[n] * B.zs;
+  float logp = fmaf(zy, B.zs, -B.lse[n]), om = -expm1f(logp);
+  if (B.logp && om < 0.0625f) {
+    logp = B.logp[n];
+    om = -expm1f(logp);
+  }
   c.bias = B.lse[n] * kLog2e;
   if (!B.dent) {
-    const float room = om < 9.31e-10f ? 9.31e-10f : om;       // 2^-30: 1 - pl of a label whose p rounds to 1; NaN stays
+    const float room = om < 5.42e-20f ? 5.42e-20f : om;       // 2^-64, for a division; NaN stays
     scale = -g * room;
     c.bias += log2f(room);
     c.a = c.b = 0.f;
@@ -305,13 +314,19 @@ gather_live_kernel(const uint4* __restrict__ src, int d8, const int32_t* __restr
 }
 
 // Forward: running scaled maximum and sum-exp over the unit's vocabulary
-// columns, the label's logit, and with ENT the sum of e u that the entropy
+// columns but the label's, and with ENT the sum of e u that the entropy
 // needs.  In log2 units, u_v = z_v zl2 - mb with zl2 = log2(e) / T (times
 // accumulation_gain) and mb = max z * zl2 as rounded: s = sum 2^u and
 // t = sum 2^u u (u <= 0, so t does not cancel).  A new maximum shifts u by
 // delta = mb_old - mb_new: t <- 2^delta (t + delta s), s <- 2^delta s.
-// Partials (mb, s, t, label logit) per live row and column range; columns >= V
-// are taken as -1e30.
+// The label's own term comes in when all others are summed, from its exact
+// logit (logp_merge_kernel): beside a label of probability one the others would
+// be lost in an fp32 sum that holds it, and log p with them.
+// Partials {mb, s, t, -} per live row and column range.  The label's column and
+// columns >= V are taken as kNoLogit; the maximum starts far above it and below
+// any logit, so that u is finite and 2^u 0 in a range without other columns.
+constexpr float kNoLogit = -1e30f, kLeastMax = -1e29f;
+
 template <bool ENT>
 struct EpiLogp {
   static constexpr bool kStaging = false;
@@ -319,18 +334,17 @@ struct EpiLogp {
     int V;
     float zl2;
     const int32_t* lab;
-    float *part_m, *part_s, *part_t, *part_g;
+    float4* part;
   };
-  float mrun, srun, trun, grun;
+  float mrun, srun, trun;
   int grow, rows, label;
 
   __device__ __forceinline__ void begin_unit(const Params& P, int grow_, int, int, const EpiCtx& cx) {
     grow = grow_;
     rows = cx.rows_valid;
-    mrun = -INFINITY;
+    mrun = kLeastMax;
     srun = 0.f;
     trun = 0.f;
-    grun = 0.f;
     label = grow < rows ? P.lab[grow] : -1;
   }
 
@@ -345,9 +359,14 @@ struct EpiLogp {
       if (c0 + 64 > P.V) {
 #pragma unroll
         for (int i = 0; i < 64; ++i)
-          if (c0 + i >= P.V) v[i] = -1e30f;
+          if (c0 + i >= P.V) v[i] = kNoLogit;
       }
-      if (label >= c0 && label < c0 + 64) grun = pick64(v, label - c0);     // once per row
+      const int off = label - c0;
+      if ((unsigned)off < 64u) {              // once per row
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (i == off) v[i] = kNoLogit;
+      }
       float t[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) t[i] = fmaxf(v[i], v[i + 32]);
@@ -385,25 +404,19 @@ struct EpiLogp {
   }
 
   __device__ __forceinline__ void end_unit(const Params& P, int, int split) {
-    if (grow < rows) {
-      const size_t o = (size_t)split * rows + grow;
-      P.part_m[o] = mrun * P.zl2;
-      P.part_s[o] = srun;
-      P.part_g[o] = grun;
-      if (ENT) P.part_t[o] = trun;
-    }
+    if (grow < rows) P.part[(size_t)split * rows + grow] = make_float4(mrun * P.zl2, srun, trun, 0.f);
   }
 };
 
 // A row's state over some of the columns: m (the scaled maximum mb of
-// EpiLogp), s, t and the label's logit, 0 where the columns do not hold it.
+// EpiLogp), s and t.
 template <bool ENT>
 struct LogpState {
-  float m, s, t, g;
+  float m, s, t;
 
   __device__ __forceinline__ void clear() {
     m = -INFINITY;
-    s = t = g = 0.f;
+    s = t = 0.f;
   }
   __device__ __forceinline__ void join(const LogpState& o) {
     const float top = fmaxf(m, o.m);
@@ -411,7 +424,6 @@ struct LogpState {
     const float f1 = ex2_approx(d1), f2 = ex2_approx(d2);
     if (ENT) t = (f1 > 0.f ? f1 * fmaf(d1, s, t) : 0.f) + (f2 > 0.f ? f2 * fmaf(d2, o.s, o.t) : 0.f);
     s = fmaf(f1, s, f2 * o.s);
-    g += o.g;
     m = top;
   }
   // One more column's logit.
@@ -432,30 +444,33 @@ struct LogpState {
     r.m = __shfl_xor_sync(0xffffffffu, m, o);
     r.s = __shfl_xor_sync(0xffffffffu, s, o);
     r.t = ENT ? __shfl_xor_sync(0xffffffffu, t, o) : 0.f;
-    r.g = __shfl_xor_sync(0xffffffffu, g, o);
     return r;
   }
 };
 
-// Joins the column ranges' partials of a row.
-// The label's term is then exchanged for that of its exact logit z_y (see
-// gather_live_kernel; the products' own g serves to take the old term out):
-// with u = g zl2 - M, u' = z_y log2(e) / T - M,
-//   s <- s + 2^u (2^(u' - u) - 1),  t <- t + 2^u' u' - 2^u u.
-// With M the largest scaled maximum,
-//   logp = ln 2 (u' - log2 s),  lse = ln 2 (M + log2 s),
-//   ent = ln 2 (log2 s - t / s):
-// the label's logit meets M before the logarithm is added, so that a
-// confident token's small log-probability is not the rest of two large terms.
+__device__ __forceinline__ bool status_timed_out(const Status* s) {
+  return *reinterpret_cast<const volatile unsigned int*>(&s->timeout) != 0u;
+}
+
+// Joins the column ranges' partials of a row, then takes in the label's term,
+// from its exact logit z_y (see gather_live_kernel).  With M the others' scaled
+// maximum, s and t their sums, and u = z_y log2(e) / T - M:
+//   u < 0:  S = s + 2^u,  logp = ln 2 (u - log2 S),  lse = ln 2 (M + log2 S),
+//           ent = ln 2 (log2 S - (t + 2^u u) / S)
+//   u >= 0: over the label's term, r = 2^-u s (the others' sum),
+//           logp = -log(1 + r),  lse = z_y / T + log(1 + r),
+//           ent = log(1 + r) - ln 2 2^-u (t - u s) / (1 + r):
+// a confident token's log-probability, -r as r goes to 0, keeps its relative
+// precision, and with it 1 - p.  It is written a second time (`kept`, may be
+// null) for the gradient: the first is the caller's to change.
 //
 // ROWS rows a block, LANES threads a row: 32 and 8 for the GEMM's few ranges,
 // one row and 256 threads for the many of logp_few_kernel.
 template <bool ENT, int ROWS, int LANES>
 __global__ void __launch_bounds__(ROWS * LANES)
-logp_merge_kernel(const float* __restrict__ part_m, const float* __restrict__ part_s, const float* __restrict__ part_t,
-                  const float* __restrict__ part_g, const LiveRows* __restrict__ live,
-                  const int32_t* __restrict__ rowmap, const float* __restrict__ zlab, float zl2, float zl2_exact,
-                  float* __restrict__ logp, float* __restrict__ lse, float* __restrict__ ent,
+logp_merge_kernel(const float4* __restrict__ part, const LiveRows* __restrict__ live,
+                  const int32_t* __restrict__ rowmap, const float* __restrict__ zlab, float zl2_exact,
+                  float* __restrict__ logp, float* __restrict__ kept, float* __restrict__ lse, float* __restrict__ ent,
                   const Status* __restrict__ status) {
   __shared__ LogpState<ENT> s_part[LANES][ROWS];
   wait_previous();
@@ -466,13 +481,8 @@ logp_merge_kernel(const float* __restrict__ part_m, const float* __restrict__ pa
   st.clear();
   if (q < rows)
     for (int k = y; k < splits; k += LANES) {
-      const size_t o = (size_t)k * rows + q;
-      LogpState<ENT> other;
-      other.m = part_m[o];
-      other.s = part_s[o];
-      other.t = ENT ? part_t[o] : 0.f;
-      other.g = part_g[o];
-      st.join(other);
+      const float4 p = part[(size_t)k * rows + q];
+      st.join(LogpState<ENT>{p.x, p.y, p.z});
     }
   s_part[y][x] = st;
 #pragma unroll
@@ -485,18 +495,24 @@ logp_merge_kernel(const float* __restrict__ part_m, const float* __restrict__ pa
   }
   if (y == 0 && q < rows) {
     const int n = rowmap[q];
-    const float ug = fmaf(st.g, zl2, -st.m), uy = fmaf(zlab[q], zl2_exact, -st.m);
-    const float eg = exp2f(ug), more = eg * expm1f((uy - ug) * kLn2);
-    st.s += more;
-    const float l2 = log2f(st.s);
-    const bool failed = *reinterpret_cast<const volatile unsigned int*>(&status->timeout) != 0u;
-    const float nan = __int_as_float(0x7fc00000);
-    logp[n] = failed ? nan : kLn2 * (uy - l2);
-    lse[n] = failed ? nan : kLn2 * (st.m + l2);
-    if (ENT) {
-      st.t += fmaf(more, uy, eg * (uy - ug));
-      ent[n] = failed ? nan : kLn2 * (l2 - st.t / st.s);
+    const float zy = zlab[q] * zl2_exact, u = fmaf(zlab[q], zl2_exact, -st.m);
+    float lp, ls, en;
+    if (u >= 0.f) {
+      const float f = exp2f(-u), r = f * st.s, l = log1pf(r);
+      lp = -l;
+      ls = fmaf(kLn2, zy, l);
+      en = f > 0.f ? l - kLn2 * f * fmaf(-u, st.s, st.t) / (1.f + r) : l;
+    } else {                                  // NaN too
+      const float e = exp2f(u), s = st.s + e, l2 = log2f(s);
+      lp = kLn2 * (u - l2);
+      ls = kLn2 * (st.m + l2);
+      en = kLn2 * (l2 - (e > 0.f ? fmaf(e, u, st.t) : st.t) / s);
     }
+    if (status_timed_out(status)) lp = ls = en = __int_as_float(0x7fc00000);
+    logp[n] = lp;
+    lse[n] = ls;
+    if (kept) kept[n] = lp;
+    if (ENT) ent[n] = en;
   }
 }
 
@@ -543,7 +559,8 @@ struct FewArgs {
   int32_t* rowmap;
   LiveRows* live;
   Status* status;
-  float *zlab, *part_m, *part_s, *part_t, *part_g;
+  float* zlab;
+  float4* part;
 };
 
 __device__ __forceinline__ void mma_m16n8k16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -661,10 +678,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) logp_few_kernel(
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         LogpState<ENT>& x = st[2 * nt + j];
-        if (ra < r1) x.add(z[nt][j], A.zl2);
-        if (rb < r1) x.add(z[nt][j + 2], A.zl2);
-        if (lab[2 * nt + j] == ra && ra < r1) x.g = z[nt][j];
-        if (lab[2 * nt + j] == rb && rb < r1) x.g = z[nt][j + 2];
+        if (ra < r1 && ra != lab[2 * nt + j]) x.add(z[nt][j], A.zl2);
+        if (rb < r1 && rb != lab[2 * nt + j]) x.add(z[nt][j + 2], A.zl2);
       }
   };
   auto step = [&](int& r, int& k0) {          // to the next batch
@@ -701,11 +716,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) logp_few_kernel(
   if (n < rows) {
     LogpState<ENT> x = s_part[0][n];
     for (int k = 1; k < kFewWarps; ++k) x.join(s_part[k][n]);
-    const size_t o = (size_t)blockIdx.x * rows + n;
-    A.part_m[o] = x.m;
-    A.part_s[o] = x.s;
-    A.part_g[o] = x.g;
-    if (ENT) A.part_t[o] = x.t;
+    A.part[(size_t)blockIdx.x * rows + n] = make_float4(x.m, x.s, x.t, 0.f);
   }
 }
 

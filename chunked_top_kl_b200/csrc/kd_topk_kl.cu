@@ -874,7 +874,7 @@ LogpLayout make_logp_layout(int64_t N, int64_t d, int64_t V, int64_t chunk, bool
   L.off_lab = take(sizeof(int32_t) * (size_t)n);
   if (!backward) {
     L.slots = logp_part_slots(n);
-    L.off_part = take(4 * sizeof(float) * (size_t)L.slots);
+    L.off_part = take(sizeof(float4) * (size_t)L.slots);
     L.off_wave = take(sizeof(unsigned int) * (size_t)wave_slots_bound(logp_units_bound(n), 0));
     L.off_zlab = take(sizeof(float) * (size_t)n);
     L.off_hc = take(2 * (size_t)(n > kPadRows ? n : kPadRows) * d);
@@ -925,8 +925,8 @@ constexpr int64_t kSingleRows = 128;
 constexpr int kSingleMaxSplits = 160;       // column ranges of the one band: a range for every SM
 
 template <bool ENT>
-int logp_forward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, float T, float* logp, float* lse,
-                 float* ent, const LogpLayout& L, void* ws, int dev, cudaStream_t s, LabelPrep lp) {
+int logp_forward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, float T, float* logp, float* kept,
+                 float* lse, float* ent, const LogpLayout& L, void* ws, int dev, cudaStream_t s, LabelPrep lp) {
   const bool single = N <= kSingleRows;      // 128-row tiles of one CTA each
   const int groups = single ? device_sms(dev) : resident_groups(dev);
   const int64_t n_tiles = ceil_div(V, BN), most = ceil_div(N, GeoP::TILE_M) * n_tiles;
@@ -964,11 +964,7 @@ int logp_forward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, 
   ep.V = (int)V;
   ep.zl2 = (float)(1.4426950408889634 / T * accumulation_gain(d));
   ep.lab = lp.lab;
-  float* part = at<float>(ws, L.off_part);
-  ep.part_m = part;
-  ep.part_s = part + L.slots;
-  ep.part_g = part + 2 * L.slots;
-  ep.part_t = part + 3 * L.slots;
+  ep.part = at<float4>(ws, L.off_part);
   const DynRows dyn{&live->count, 0, (int)N, &live->raster};
   cudaError_t e;
   if (single) {
@@ -983,15 +979,15 @@ int logp_forward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, 
     e = launch_one<ProbLogp<ENT>>(ENT ? 5 : 4, dev, lp.groups, tmH, tmW, tmH, a, lp.status, ep, s, dyn, wave, true);
   }
   if (e != cudaSuccess) return KD_ERR_CUDA;
-  return launch_next(logp_merge_kernel<ENT, 32, 8>, (unsigned)ceil_div(N, 32), 256u, s, ep.part_m, ep.part_s, ep.part_t,
-                     ep.part_g, live, lp.rowmap, zlab, ep.zl2, kLog2e / T, logp, lse, ent, lp.status) == cudaSuccess
+  return launch_next(logp_merge_kernel<ENT, 32, 8>, (unsigned)ceil_div(N, 32), 256u, s, ep.part, live, lp.rowmap, zlab,
+                     kLog2e / T, logp, kept, lse, ent, lp.status) == cudaSuccess
              ? KD_OK
              : KD_ERR_CUDA;
 }
 
 template <bool ENT>
 int logp_forward_few(const void* H, const void* W, const void* labels, int labels_i64, int64_t N, int64_t d, int64_t V,
-                     float T, float* logp, float* lse, float* ent, const LogpLayout& L, void* ws, int dev,
+                     float T, float* logp, float* kept, float* lse, float* ent, const LogpLayout& L, void* ws, int dev,
                      cudaStream_t s) {
   FewArgs a{};
   a.H = static_cast<const uint4*>(H);
@@ -1009,11 +1005,7 @@ int logp_forward_few(const void* H, const void* W, const void* labels, int label
   a.live = at<LiveRows>(ws, L.off_live);
   a.status = at<Status>(ws, L.off_status);
   a.zlab = at<float>(ws, L.off_zlab);
-  float* part = at<float>(ws, L.off_part);
-  a.part_m = part;
-  a.part_s = part + L.slots;
-  a.part_g = part + 2 * L.slots;
-  a.part_t = part + 3 * L.slots;
+  a.part = at<float4>(ws, L.off_part);
   // a range of at least 16 rows for each warp, and a partial slot for each block and token
   int64_t blocks = (int64_t)device_sms(dev) * kFewBlocksPerSm, want = ceil_div(V, 16 * kFewWarps);
   if (blocks > want) blocks = want;
@@ -1029,16 +1021,16 @@ int logp_forward_few(const void* H, const void* W, const void* labels, int label
   }
   kern<<<grid, kFewThreads, (size_t)few_smem(N, d), s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return KD_ERR_CUDA;
-  return launch_next(logp_merge_kernel<ENT, 1, 256>, (unsigned)N, 256u, s, a.part_m, a.part_s, a.part_t, a.part_g, a.live,
-                     a.rowmap, a.zlab, a.zl2, a.zl2, logp, lse, ent, a.status) == cudaSuccess
+  return launch_next(logp_merge_kernel<ENT, 1, 256>, (unsigned)N, 256u, s, a.part, a.live, a.rowmap, a.zlab, a.zl2, logp,
+                     kept, lse, ent, a.status) == cudaSuccess
              ? KD_OK
              : KD_ERR_CUDA;
 }
 
 template <bool ENT>
 int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, float T, const float* lse,
-                  const float* ent, const float* dlogp, const float* dent, void* dH, void* dW, bool half_dW,
-                  bool accumulate_dW, const LogpLayout& L, void* ws, int dev, cudaStream_t s, LabelPrep lp) {
+                  const float* logp, const float* ent, const float* dlogp, const float* dent, void* dH, void* dW,
+                  bool half_dW, bool accumulate_dW, const LogpLayout& L, void* ws, int dev, cudaStream_t s, LabelPrep lp) {
   const int groups = resident_groups(dev);
   const int64_t n_tiles = ceil_div(V, BN), C = L.C;
   const int64_t most = ceil_div(C, GeoP::TILE_M) * n_tiles;
@@ -1086,7 +1078,7 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
     const int64_t want = ceil_div(Cc, 8);
     const unsigned blocks = (unsigned)(want < copy_blocks ? want : copy_blocks);
     unsigned int* wave = with_dW ? jwave + (size_t)(c0 / C) * L.jwave_per_chunk : nullptr;
-    RowScales rs{lse, ent, dlogp, dent, 1.0f / T, coef, scale, with_dW ? static_cast<uint4*>(hs) : nullptr,
+    RowScales rs{lse, ent, dlogp, dent, logp, 1.0f / T, coef, scale, with_dW ? static_cast<uint4*>(hs) : nullptr,
                  static_cast<uint4*>(dH), c0 == 0 ? N * (d / 8) : 0, wave, wave ? L.jwave_per_chunk : 0};
     if (launch_next(gather_live_kernel<true>, blocks, 256u, s, static_cast<const uint4*>(H), (int)(d / 8), lp.rowmap, live,
                     (int)c0, (int)Cc, static_cast<uint4*>(hc), static_cast<const uint4*>(W), lp.lab, nullptr, rs) !=
@@ -1192,10 +1184,18 @@ size_t kd_token_logp_backward_workspace_size(int64_t N, int64_t d, int64_t V, in
 int kd_token_logp_forward(const void* H, const void* W, const void* labels, int labels_i64, int64_t N, int64_t d,
                           int64_t V, float T, float* logp, float* lse, float* entropy, void* workspace,
                           size_t workspace_bytes, void* stream) {
+  return kd_token_logp_forward_ex(H, W, labels, labels_i64, N, d, V, T, logp, lse, entropy, nullptr, workspace,
+                                  workspace_bytes, stream);
+}
+
+int kd_token_logp_forward_ex(const void* H, const void* W, const void* labels, int labels_i64, int64_t N, int64_t d,
+                             int64_t V, float T, float* logp, float* lse, float* entropy, float* logp_kept,
+                             void* workspace, size_t workspace_bytes, void* stream) {
   int st = logp_common(H, W, labels, labels_i64, N, d, V, T, 1, workspace);
   if (st != KD_OK) return st;
   if (N > 0 && (!logp || !lse)) return KD_ERR_INVALID_ARG;
-  if (!aligned(logp, 4) || !aligned(lse, 4) || !aligned(entropy, 4)) return KD_ERR_INVALID_ARG;
+  for (const float* p : {logp, lse, entropy, logp_kept})
+    if (!aligned(p, 4)) return KD_ERR_INVALID_ARG;
   const LogpLayout L = make_logp_layout(N, d, V, 1, false, false);
   if (workspace_bytes < L.total) return KD_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1205,23 +1205,33 @@ int kd_token_logp_forward(const void* H, const void* W, const void* labels, int 
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KD_ERR_CUDA;
   if ((N <= 8 || (N <= kFewTokens && 2 * V * d <= kFewWideBytes)) && few_smem(N, d) <= kFewSmem)
-    return entropy ? logp_forward_few<true>(H, W, labels, labels_i64, N, d, V, T, logp, lse, entropy, L, workspace, dev, s)
-                   : logp_forward_few<false>(H, W, labels, labels_i64, N, d, V, T, logp, lse, nullptr, L, workspace, dev, s);
+    return entropy ? logp_forward_few<true>(H, W, labels, labels_i64, N, d, V, T, logp, logp_kept, lse, entropy, L,
+                                            workspace, dev, s)
+                   : logp_forward_few<false>(H, W, labels, labels_i64, N, d, V, T, logp, logp_kept, lse, nullptr, L,
+                                             workspace, dev, s);
   const LabelPrep lp = label_prep(labels, labels_i64, N, V, L, workspace);
-  return entropy ? logp_forward<true>(H, W, N, d, V, T, logp, lse, entropy, L, workspace, dev, s, lp)
-                 : logp_forward<false>(H, W, N, d, V, T, logp, lse, nullptr, L, workspace, dev, s, lp);
+  return entropy ? logp_forward<true>(H, W, N, d, V, T, logp, logp_kept, lse, entropy, L, workspace, dev, s, lp)
+                 : logp_forward<false>(H, W, N, d, V, T, logp, logp_kept, lse, nullptr, L, workspace, dev, s, lp);
 }
 
 int kd_token_logp_backward(const void* H, const void* W, const void* labels, int labels_i64, int64_t N, int64_t d,
                            int64_t V, float T, int64_t chunk, const float* lse, const float* entropy,
                            const float* dlogp, const float* dentropy, void* dH, void* dW, int dW_bf16,
                            int accumulate_dW, void* workspace, size_t workspace_bytes, void* stream) {
+  return kd_token_logp_backward_ex(H, W, labels, labels_i64, N, d, V, T, chunk, lse, entropy, nullptr, dlogp, dentropy,
+                                   dH, dW, dW_bf16, accumulate_dW, workspace, workspace_bytes, stream);
+}
+
+int kd_token_logp_backward_ex(const void* H, const void* W, const void* labels, int labels_i64, int64_t N, int64_t d,
+                              int64_t V, float T, int64_t chunk, const float* lse, const float* entropy,
+                              const float* logp, const float* dlogp, const float* dentropy, void* dH, void* dW,
+                              int dW_bf16, int accumulate_dW, void* workspace, size_t workspace_bytes, void* stream) {
   int st = logp_common(H, W, labels, labels_i64, N, d, V, T, chunk, workspace);
   if (st != KD_OK) return st;
   if ((dW_bf16 & ~1) || (dW_bf16 && accumulate_dW)) return KD_ERR_INVALID_ARG;
   if (N > 0 && (!lse || !dlogp || !dH || (dentropy && !entropy))) return KD_ERR_INVALID_ARG;
   if (!aligned(dH, 16) || !aligned(dW, 16)) return KD_ERR_INVALID_ARG;
-  for (const float* p : {lse, entropy, dlogp, dentropy})
+  for (const float* p : {lse, entropy, logp, dlogp, dentropy})
     if (!aligned(p, 4)) return KD_ERR_INVALID_ARG;
   const LogpLayout L = make_logp_layout(N, d, V, chunk, true, dW_bf16 != 0);
   if (workspace_bytes < L.total) return KD_ERR_WORKSPACE;
@@ -1235,9 +1245,9 @@ int kd_token_logp_backward(const void* H, const void* W, const void* labels, int
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KD_ERR_CUDA;
   const LabelPrep lp = label_prep(labels, labels_i64, N, V, L, workspace);
-  return dentropy ? logp_backward<true>(H, W, N, d, V, T, lse, entropy, dlogp, dentropy, dH, dW, dW_bf16 != 0,
+  return dentropy ? logp_backward<true>(H, W, N, d, V, T, lse, logp, entropy, dlogp, dentropy, dH, dW, dW_bf16 != 0,
                                         accumulate_dW != 0, L, workspace, dev, s, lp)
-                  : logp_backward<false>(H, W, N, d, V, T, lse, entropy, dlogp, nullptr, dH, dW, dW_bf16 != 0,
+                  : logp_backward<false>(H, W, N, d, V, T, lse, logp, entropy, dlogp, nullptr, dH, dW, dW_bf16 != 0,
                                          accumulate_dW != 0, L, workspace, dev, s, lp);
 }
 

@@ -50,6 +50,11 @@ def token_logprobs_forward(H, W, labels, T: float = 1.0, entropy: bool = False,
     z = H W^T / T, lse = log sum exp z, logp = z[label] - lse and the entropy
     of softmax(z).  All are 0 where the label is negative; a label >= V gives
     NaN and is counted for ``check(workspace)``."""
+    return _forward(H, W, labels, T, entropy, workspace, None)
+
+
+def _forward(H, W, labels, T, entropy, workspace, kept):
+    """token_logprobs_forward; logp is also written to ``kept``, if any."""
     where = "token_logprobs"
     N, d, V = _check(where, H, W, labels)
     dev = H.device
@@ -64,10 +69,10 @@ def token_logprobs_forward(H, W, labels, T: float = 1.0, entropy: bool = False,
     lse = torch.empty_like(logp)
     ent = torch.empty_like(logp) if entropy else None
     with _on(dev):
-        st = _abi.kd_token_logp_forward(_ptr(H), _ptr(W), _ptr(labels), int(labels.dtype == torch.int64), N, d, V,
-                                        float(T), _ptr(logp), _ptr(lse), _ptr(ent), _ptr(workspace), workspace.numel(),
-                                        _stream(dev))
-    _raise(st, "kd_token_logp_forward")
+        st = _abi.kd_token_logp_forward_ex(_ptr(H), _ptr(W), _ptr(labels), int(labels.dtype == torch.int64), N, d, V,
+                                           float(T), _ptr(logp), _ptr(lse), _ptr(ent), _ptr(kept), _ptr(workspace),
+                                           workspace.numel(), _stream(dev))
+    _raise(st, "kd_token_logp_forward_ex")
     return logp, lse, ent
 
 
@@ -75,20 +80,23 @@ def token_logprobs_backward(H, W, labels, lse, dlogp, T: float = 1.0, chunk: int
                             entropy: Optional[torch.Tensor] = None, dentropy: Optional[torch.Tensor] = None,
                             dW: Optional[torch.Tensor] = None, accumulate_dW: bool = False,
                             dW_dtype: Optional[torch.dtype] = torch.float32,
-                            workspace: Optional[torch.Tensor] = None
+                            workspace: Optional[torch.Tensor] = None, logp: Optional[torch.Tensor] = None
                             ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Returns (dH [N,d] bf16, dW [V,d]) for the upstream gradients ``dlogp``
     and, with ``entropy`` from the forward pass, ``dentropy``.  ``dW_dtype`` is
     float32, bfloat16 (rounded once, at the end) or None for dH alone; a given
     ``dW`` decides its own type, and a float32 one can be added to
     (``accumulate_dW``).  ``lse`` must come from the forward pass with the same
-    inputs; ``chunk`` tokens' dZ rows are held at once."""
+    inputs, and ``logp`` too: with it the 1 - p of a label that the head is
+    nearly sure of keeps its relative precision, without it 1 - p is known to
+    about 1e-6 (the rounding of lse).  ``chunk`` tokens' dZ rows are held at
+    once."""
     where = "token_logprobs_backward"
     N, d, V = _check(where, H, W, labels)
     dev = H.device
     if (entropy is None) != (dentropy is None):
         raise ValueError(f"{where}: entropy and dentropy come together")
-    for name, t in (("lse", lse), ("dlogp", dlogp), ("entropy", entropy), ("dentropy", dentropy)):
+    for name, t in (("lse", lse), ("logp", logp), ("dlogp", dlogp), ("entropy", entropy), ("dentropy", dentropy)):
         if t is not None:
             _check_buffer(t, name, (N,), torch.float32, dev)
     if dW is not None:
@@ -101,10 +109,10 @@ def token_logprobs_backward(H, W, labels, lse, dlogp, T: float = 1.0, chunk: int
         _check_buffer(dW, "dW", (V, d), dW_dtype, dev)
     if workspace is not None:
         _check_workspace(workspace, dev)
-    return _backward(H, W, labels, lse, dlogp, T, chunk, entropy, dentropy, dW, accumulate_dW, dW_dtype, workspace)
+    return _backward(H, W, labels, lse, logp, dlogp, T, chunk, entropy, dentropy, dW, accumulate_dW, dW_dtype, workspace)
 
 
-def _backward(H, W, labels, lse, dlogp, T, chunk, entropy, dentropy, dW, accumulate_dW, dW_dtype, workspace):
+def _backward(H, W, labels, lse, logp, dlogp, T, chunk, entropy, dentropy, dW, accumulate_dW, dW_dtype, workspace):
     """token_logprobs_backward on checked arguments."""
     N, d = H.shape
     V = W.shape[0]
@@ -119,19 +127,21 @@ def _backward(H, W, labels, lse, dlogp, T, chunk, entropy, dentropy, dW, accumul
             raise ValueError("token_logprobs_backward: unsupported sizes")
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     with _on(dev):
-        st = _abi.kd_token_logp_backward(_ptr(H), _ptr(W), _ptr(labels), int(labels.dtype == torch.int64), N, d, V,
-                                         float(T), int(chunk), _ptr(lse), _ptr(entropy), _ptr(dlogp), _ptr(dentropy),
-                                         _ptr(dH), _ptr(dW), half, int(bool(accumulate_dW)), _ptr(workspace),
-                                         workspace.numel(), _stream(dev))
-    _raise(st, "kd_token_logp_backward")
+        st = _abi.kd_token_logp_backward_ex(_ptr(H), _ptr(W), _ptr(labels), int(labels.dtype == torch.int64), N, d, V,
+                                            float(T), int(chunk), _ptr(lse), _ptr(entropy), _ptr(logp), _ptr(dlogp),
+                                            _ptr(dentropy), _ptr(dH), _ptr(dW), half, int(bool(accumulate_dW)),
+                                            _ptr(workspace), workspace.numel(), _stream(dev))
+    _raise(st, "kd_token_logp_backward_ex")
     return dH, dW
 
 
 class TokenLogprobsFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, H, W, labels, T, chunk, entropy):
-        logp, lse, ent = token_logprobs_forward(H, W, labels, T, entropy)
-        ctx.save_for_backward(H, W, labels, lse, ent)
+        # the gradient's own copy of logp: the one returned may be changed in place
+        kept = torch.empty(labels.shape, dtype=torch.float32, device=H.device) if any(ctx.needs_input_grad) else None
+        logp, lse, ent = _forward(H, W, labels, T, entropy, None, kept)
+        ctx.save_for_backward(H, W, labels, lse, kept, ent)
         ctx.T, ctx.chunk = T, chunk
         ctx.set_materialize_grads(False)
         return (logp, ent) if entropy else logp
@@ -141,13 +151,13 @@ class TokenLogprobsFunction(torch.autograd.Function):
     def backward(ctx, dlogp, dent=None):
         if dlogp is None and dent is None:
             return (None,) * 6
-        H, W, labels, lse, ent = ctx.saved_tensors
+        H, W, labels, lse, logp, ent = ctx.saved_tensors
         dlogp = torch.zeros_like(lse) if dlogp is None else dlogp.contiguous()
         if dent is None:                # the entropy took no part in the loss
             ent = None
         else:
             dent = dent.contiguous()
-        dH, dW = _backward(H, W, labels, lse, dlogp, ctx.T, ctx.chunk, ent, dent, None, False,
+        dH, dW = _backward(H, W, labels, lse, logp, dlogp, ctx.T, ctx.chunk, ent, dent, None, False,
                            W.dtype if ctx.needs_input_grad[1] else None, None)
         return dH, dW, None, None, None, None
 

@@ -286,12 +286,20 @@ int kd_teacher_topk(const void* Ht, const void* Wt, int64_t N, int64_t d, int64_
  * counted in the workspace and reported by kd_topk_kl_check as
  * KD_ERR_BAD_INDEX.  The tokens with a label are gathered on the device (N x d
  * bf16 of workspace); no logits are stored.  When a pipeline wait times out
- * the outputs are NaN. */
+ * the outputs are NaN.  logp and the entropy keep their relative precision
+ * where a label's probability is nearly 1 (the label's term is left out of the
+ * sum of the others).  kd_token_logp_forward_ex writes the labelled tokens'
+ * logp to logp_kept [N] as well (NULL for none), for a gradient computed after
+ * logp has been changed. */
 size_t kd_token_logp_forward_workspace_size(int64_t N, int64_t d, int64_t V);
 int kd_token_logp_forward(const void* H, const void* W, const void* labels, int labels_i64,
                           int64_t N, int64_t d, int64_t V, float T,
                           float* logp, float* lse, float* entropy,
                           void* workspace, size_t workspace_bytes, void* stream);
+int kd_token_logp_forward_ex(const void* H, const void* W, const void* labels, int labels_i64,
+                             int64_t N, int64_t d, int64_t V, float T,
+                             float* logp, float* lse, float* entropy, float* logp_kept,
+                             void* workspace, size_t workspace_bytes, void* stream);
 
 /* Gradients of the above for upstream gradients dlogp[N] and dentropy[N]
  * (NULL for none; otherwise entropy must be the forward pass's output):
@@ -300,7 +308,11 @@ int kd_token_logp_forward(const void* H, const void* W, const void* labels, int 
  *   dH = dZ W (bf16 [N][d], overwritten),  dW = dZ^T H
  * with p recomputed from lse, `chunk` tokens at a time.  Before the two
  * products dZ is rounded to bf16, each row over a scale that makes the label's
- * entry exact; dH takes the scale in fp32, dW with H (rounded to bf16 again).  Tokens without a valid label and tokens whose
+ * entry +-1 without rounding; dH takes the scale in fp32, dW with H (rounded to
+ * bf16 again).  The label's entry holds 1 - p[label]: from the forward pass's
+ * logp (kd_token_logp_backward_ex) to a relative 2^-13 or better, from lse alone
+ * (logp NULL, or kd_token_logp_backward) to the rounding of lse, about 1e-6.
+ * Tokens without a valid label and tokens whose
  * upstream gradients are 0 are left out (their dH rows are 0).  dW is fp32
  * [V][d] (overwritten, or added to with accumulate_dW = 1), or bf16 [V][d]
  * with dW_bf16 = 1 (overwritten; rounded once, after the sum over all
@@ -312,6 +324,12 @@ int kd_token_logp_backward(const void* H, const void* W, const void* labels, int
                            const float* dlogp, const float* dentropy,
                            void* dH, void* dW, int dW_bf16, int accumulate_dW,
                            void* workspace, size_t workspace_bytes, void* stream);
+int kd_token_logp_backward_ex(const void* H, const void* W, const void* labels, int labels_i64,
+                              int64_t N, int64_t d, int64_t V, float T, int64_t chunk,
+                              const float* lse, const float* entropy, const float* logp,
+                              const float* dlogp, const float* dentropy,
+                              void* dH, void* dW, int dW_bf16, int accumulate_dW,
+                              void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * Losses over token log-probabilities.  The arrays are fp32 [N], the tokens
