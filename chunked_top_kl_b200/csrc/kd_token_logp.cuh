@@ -810,12 +810,27 @@ struct EpiDhPart {
 };
 
 // dH[token] = bf16(scale * sum over the K ranges, in order) for the chunk's live
-// rows; eight values a thread.  `full` is the plan of a chunk that is live throughout.
+// rows; eight values a thread.  `full_splits` is the plan of a chunk that is live
+// throughout.  When a pipeline wait of the call has given up, the last chunk's
+// launch writes NaN to all of dH and dW instead (Gradients, null before the
+// last): in a training step nobody reads the status words.
+struct Gradients {
+  uint4 *dH, *dW;           // dW null: none wanted
+  int64_t dH_n, dW_n;       // 16-byte vectors
+};
+
 __global__ void __launch_bounds__(256)
 dh_finish_kernel(const float4* __restrict__ part, int d8, const int32_t* __restrict__ rowmap,
                  const LiveRows* __restrict__ live, const float* __restrict__ scale, int row0, int C, int full_splits,
-                 uint4* __restrict__ dH) {
+                 uint4* __restrict__ dH, const Status* status, const Gradients all) {
   wait_previous();
+  if (status_timed_out(status)) {
+    const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+    const uint32_t nan = 0x7fc07fc0u;         // two bf16 NaN, and an fp32 one
+    for (int64_t i = i0; i < all.dH_n; i += step) all.dH[i] = make_uint4(nan, nan, nan, nan);
+    for (int64_t i = i0; i < all.dW_n; i += step) all.dW[i] = make_uint4(nan, nan, nan, nan);
+    return;
+  }
   int rows = live->count - row0;
   rows = rows < 0 ? 0 : (rows > C ? C : rows);
   const int splits = rows == C ? full_splits : live->dh.k_splits;
@@ -869,9 +884,12 @@ struct EpiDwHalf {
   }
 };
 
-// out = bf16(in): the fp32 dW that several chunks added up.
-__global__ void __launch_bounds__(256) round_bf16_kernel(const float4* __restrict__ in, uint2* __restrict__ out, int64_t n4) {
+// out = bf16(in): the fp32 dW that several chunks added up; left as it is (NaN, see
+// dh_finish_kernel) when a wait has given up.
+__global__ void __launch_bounds__(256)
+round_bf16_kernel(const float4* __restrict__ in, uint2* __restrict__ out, int64_t n4, const Status* status) {
   wait_previous();
+  if (status_timed_out(status)) return;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
     const float4 f = in[i];
     out[i] = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));

@@ -1068,6 +1068,8 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
   if (with_dW && !(half_store ? make_map(&tmDW, dWacc, d, V, d, 64, BM) : make_map(&tmDW, dWacc, d, V, d, 32, BM, true)))
     return KD_ERR_CUDA;
   const unsigned copy_blocks = (unsigned)(device_sms(dev) * 8);
+  const Gradients all{static_cast<uint4*>(dH), static_cast<uint4*>(dW), N * (d / 8),
+                      with_dW ? V * (d / 8) * (half_dW ? 1 : 2) : 0};
 
   for (int64_t c0 = 0; c0 < N; c0 += C) {
     const int64_t Cc = (N - c0 < C) ? (N - c0) : C;
@@ -1143,12 +1145,12 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
     const int64_t finish = ceil_div(Cc * (d / 8), 256);
     if (launch_next(dh_finish_kernel, (unsigned)(finish < copy_blocks ? finish : copy_blocks), 256u, s,
                     reinterpret_cast<const float4*>(part32), (int)(d / 8), lp.rowmap, live, scale, (int)c0, (int)Cc,
-                    plan.k_splits, static_cast<uint4*>(dH)) != cudaSuccess)
+                    plan.k_splits, static_cast<uint4*>(dH), lp.status, c0 + C < N ? Gradients{} : all) != cudaSuccess)
       return KD_ERR_CUDA;
   }
   if (rounds) {
     if (launch_next(round_bf16_kernel, copy_blocks, 256u, s, static_cast<const float4*>(dWacc), static_cast<uint2*>(dW),
-                    V * d / 4) != cudaSuccess)
+                    V * d / 4, lp.status) != cudaSuccess)
       return KD_ERR_CUDA;
   }
   return KD_OK;

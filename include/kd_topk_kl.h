@@ -316,7 +316,9 @@ int kd_token_logp_forward_ex(const void* H, const void* W, const void* labels, i
  * upstream gradients are 0 are left out (their dH rows are 0).  dW is fp32
  * [V][d] (overwritten, or added to with accumulate_dW = 1), or bf16 [V][d]
  * with dW_bf16 = 1 (overwritten; rounded once, after the sum over all
- * chunks), or NULL: dH alone.  dH and dW must not overlap the inputs. */
+ * chunks), or NULL: dH alone.  dH and dW must not overlap the inputs.  When a
+ * pipeline wait times out all of dH and dW is NaN, what a dW given with
+ * accumulate_dW held included, and kd_topk_kl_check says so. */
 size_t kd_token_logp_backward_workspace_size(int64_t N, int64_t d, int64_t V, int64_t chunk, int dW_bf16);
 int kd_token_logp_backward(const void* H, const void* W, const void* labels, int labels_i64,
                            int64_t N, int64_t d, int64_t V, float T, int64_t chunk,
