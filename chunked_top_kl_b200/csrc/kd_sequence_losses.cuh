@@ -515,8 +515,10 @@ __device__ __forceinline__ void policy_token(const PolicyArgs& A, float lp, floa
       dk = small ? y - kl : 1.f - e;                               // 1 - e^-y
     }
   }
-  loss = fmaf(A.kl_coef, kl, -obj);
-  d = fmaf(A.kl_coef, dk, clip ? 0.f : -ra);
+  // kl_coef 0: the KL is reported and has no part in the loss, not even 0 times infinity
+  loss = KL != kNoKl && A.kl_coef != 0.f ? fmaf(A.kl_coef, kl, -obj) : -obj;
+  d = clip ? 0.f : -ra;
+  if (KL != kNoKl && A.kl_coef != 0.f) d = fmaf(A.kl_coef, dk, d);
 }
 
 // The same in 64 bits.
@@ -544,8 +546,12 @@ __device__ __forceinline__ void policy_token64(const PolicyArgs& A, float lp, fl
       kl = y - dk;
     }
   }
-  loss = A.kl_coef_64 * kl - (clip ? border * (double)a : ra);
-  d = A.kl_coef_64 * dk - (clip ? 0.0 : ra);
+  loss = -(clip ? border * (double)a : ra);
+  d = clip ? 0.0 : -ra;
+  if (KL != kNoKl && A.kl_coef_64 != 0.0) {   // 0: see policy_token
+    loss += A.kl_coef_64 * kl;
+    d += A.kl_coef_64 * dk;
+  }
 }
 
 // The blocks' partial scalars, joined in block order by one block.

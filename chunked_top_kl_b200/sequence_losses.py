@@ -165,7 +165,7 @@ def policy_loss_forward_backward(logp, old_logp, advantages, ref_logp=None, mask
     -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_coef KL; for A < 0
     ``dual_clip`` (c > 1) bounds the first term by -c A.  KL is y (``k1``),
     y^2 / 2 (``k2``) or exp(-y) - 1 + y (``k3``); without ``ref_logp`` there is
-    none.  ``advantages`` of logp's shape is per token, [S, 1] or another [S] per
+    none, and with ``kl_coef`` 0 it is reported only.  ``advantages`` of logp's shape is per token, [S, 1] or another [S] per
     sequence.  ``reduce``: ``token`` divides the weighted sum by the mask's sum;
     ``sequence`` averages each sequence over its mask, then over all S
     sequences (an empty one counts 0).  kl and clip_fraction are averaged the

@@ -378,7 +378,9 @@ int kd_preference_loss(const float* logp, const float* ref_logp, const float* ma
  * per_sequence = 1, by m_t / (S sum of its sequence's m) (a sequence whose
  * weights sum to 0 counts 0).  Writes loss[0] = sum w l, loss[1] = sum w kl,
  * loss[2] = sum w [clipped], and dlogp = g w ([not clipped] (-A r) + kl_coef
- * dkl/dlogp); old_logp, ref_logp and advantages are constants.  A token is
+ * dkl/dlogp); old_logp, ref_logp and advantages are constants.  With kl_coef 0
+ * the KL is reported only: whatever it is, infinite included, it has no part in
+ * loss[0] and dlogp.  A token is
  * clipped when A > 0 and x > log(1 + clip_high), A < 0 and
  * x < log(1 - clip_low), or A < 0 and x > log(dual_clip); a token with A = 0
  * has no first term.  0 <= clip_low < 1, clip_high >= 0. */
