@@ -207,9 +207,11 @@ class PolicyLossFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logp, old_logp, advantages, ref_logp, mask, offsets, clip_low, clip_high, dual_clip, kl_coef, kl,
                 reduce):
-        loss, kl_mean, clipped, dlogp = _policy(logp, old_logp, advantages, ref_logp, mask, offsets, clip_low,
-                                                clip_high, dual_clip, kl_coef, kl, reduce, None,
-                                                ctx.needs_input_grad[0])
+        *stats, dlogp = _policy(logp, old_logp, advantages, ref_logp, mask, offsets, clip_low, clip_high, dual_clip,
+                                kl_coef, kl, reduce, None, ctx.needs_input_grad[0])
+        # .data: tensors of their own over the three floats, not views of one, so that a caller may change the loss
+        # or a reported value in place before going backward
+        loss, kl_mean, clipped = (t.data for t in stats)
         ctx.save_for_backward(dlogp)
         ctx.mark_non_differentiable(kl_mean, clipped)
         ctx.set_materialize_grads(False)
