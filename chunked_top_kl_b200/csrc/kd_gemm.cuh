@@ -117,6 +117,10 @@ struct GemmArgs {
   // CTAs that share operand tiles keep reading them together.  Pacing only: a
   // wait gives up after kWaveWaitNs and the CTA goes on.
   unsigned int* wave_sync;
+  // A link of a chain of launches (kd_launch.cuh): follows the launch before it
+  // closely, and one that does the same comes behind it.  0 where what follows
+  // may be anyone's: it starts when this launch is over.
+  int chained;
 };
 
 constexpr uint64_t kWaveWaitNs = 20000000ull;   // 20 ms
@@ -567,8 +571,10 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__
     }
   }
   const uint32_t tmem_base = pipeline_setup<G, PAIR>(L);
-  next_may_start();
-  wait_previous();
+  if (args.chained) {
+    next_may_start();
+    wait_previous();
+  }
 
   // The schedule; a launch over a device-side row count rebuilds it here.
   GemmArgs A = args;

@@ -6,7 +6,9 @@
 // touches anything that a kernel writes, so that the last one's end is the
 // end of all.  The first of a call is an ordinary launch, and the last does not
 // let another start before its end: what follows the call may be anyone's.
-// Both calls do nothing in a kernel that was launched the ordinary way.
+// In a kernel that was launched the ordinary way wait_previous does nothing, but
+// next_may_start lets whatever follows start early: a kernel that also runs
+// outside a chain must not call it there (GemmArgs::chained).
 #pragma once
 
 #include <cuda_runtime.h>

@@ -202,7 +202,7 @@ cudaError_t launch_gemm(int slot, int dev, int groups, const CUtensorMap& ta0, c
                         const CUtensorMap& to0, const CUtensorMap& ta1, const CUtensorMap& tb1,
                         const CUtensorMap& to1, const GemmArgs& args,
                         const typename P0::Epi::Params& ep0, const typename P1::Epi::Params& ep1,
-                        cudaStream_t s, bool next = false) {
+                        cudaStream_t s) {
   using G = Geo<PAIR, P0::Epi::kStaging || P1::Epi::kStaging>;
   auto kern = gemm_tc_kernel<P0, P1, PAIR>;
   if (dev >= 0 && dev < kMaxDevices && !g_dev[dev].attr_set[slot]) {
@@ -220,10 +220,10 @@ cudaError_t launch_gemm(int slot, int dev, int groups, const CUtensorMap& ta0, c
   attr[0].val.clusterDim.x = PAIR ? 2 : 1;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // `next`: see kd_launch.cuh
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = next ? 2 : 1;
+  cfg.numAttrs = args.chained ? 2 : 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ta0, tb0, to0, ta1, tb1, to1, args, ep0, ep1);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
@@ -234,14 +234,15 @@ template <class P0>
 cudaError_t launch_one(int slot, int dev, int groups, const CUtensorMap& ta, const CUtensorMap& tb,
                        const CUtensorMap& to, const ProbArgs& pa, Status* status,
                        const typename P0::Epi::Params& ep, cudaStream_t s, DynRows dyn = DynRows{},
-                       unsigned int* wave_sync = nullptr, bool next = false) {
+                       unsigned int* wave_sync = nullptr, bool chained = false) {
   GemmArgs a{};
   a.prob[0] = pa;
   a.status = status;
   a.dyn = dyn;
   a.wave_sync = wave_sync;
+  a.chained = chained;
   EpiNone::Params none{};
-  return launch_gemm<P0, NoProb, kPair>(slot, dev, groups, ta, tb, to, ta, tb, to, a, ep, none, s, next);
+  return launch_gemm<P0, NoProb, kPair>(slot, dev, groups, ta, tb, to, ta, tb, to, a, ep, none, s);
 }
 
 // Problem 0 round-robin, problem 1 dealt to even out the groups' total K
@@ -972,9 +973,10 @@ int logp_forward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, 
     ga.prob[0] = a;
     ga.status = lp.status;
     ga.dyn = dyn;
+    ga.chained = 1;
     EpiNone::Params none{};
     e = launch_gemm<ProbLogp<ENT>, NoProb, false>(ENT ? 16 : 15, dev, lp.groups, tmH, tmW, tmH, tmH, tmW, tmH, ga, ep, none,
-                                                  s, true);
+                                                  s);
   } else {
     e = launch_one<ProbLogp<ENT>>(ENT ? 5 : 4, dev, lp.groups, tmH, tmW, tmH, a, lp.status, ep, s, dyn, wave, true);
   }
@@ -1105,6 +1107,7 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
     GemmArgs j{};
     j.status = lp.status;
     j.dyn = dyn;
+    j.chained = 1;
     const int64_t dh_bands = ceil_div(Cc, GeoP::TILE_M), k1 = with_dW ? ceil_div(Cc, BK) : 0;
     const DhPlan plan = dh_plan(dh_bands, dh_cols, d, ceil_div(V, BK), dw_units, k1, groups, L.part_rows);
     j.prob[0].raster = tile_raster(dh_bands * plan.k_splits, plan.k_cols, false);
@@ -1118,8 +1121,7 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
     cudaError_t e;
     if (!with_dW) {
       EpiNone::Params none{};
-      e = launch_gemm<ProbDhPart, NoProb, kPair>(9, dev, groups, tmZk, tmWmn, tmDH, tmZk, tmWmn, tmDH, j, eh, none, s,
-                                              true);
+      e = launch_gemm<ProbDhPart, NoProb, kPair>(9, dev, groups, tmZk, tmWmn, tmDH, tmZk, tmWmn, tmDH, j, eh, none, s);
     } else {
       j.prob[1].raster = tile_raster(ceil_div(V, GeoP::TILE_M), dh_cols, false);
       j.prob[1].num_kb = (int)ceil_div(Cc, BK);
@@ -1131,14 +1133,12 @@ int logp_backward(const void* H, const void* W, int64_t N, int64_t d, int64_t V,
       if (half_store) {
         j.prob[1].dyn_zero_fill = 1;
         EpiDwHalf::Params eb{};
-        e = launch_gemm<ProbDhPart, ProbDwHalf, kPair>(8, dev, groups, tmZk, tmWmn, tmDH, tmZmn, tmHmn, tmDW, j, eh, eb, s,
-                                                   true);
+        e = launch_gemm<ProbDhPart, ProbDwHalf, kPair>(8, dev, groups, tmZk, tmWmn, tmDH, tmZmn, tmHmn, tmDW, j, eh, eb, s);
       } else {
         EpiDw::Params ew{};
         ew.accumulate = ((accumulate_dW && !rounds) || c0 > 0) ? 1 : 0;
         j.prob[1].dyn_zero_fill = ew.accumulate ? 0 : 1;
-        e = launch_gemm<ProbDhPart, ProbDw, kPair>(10, dev, groups, tmZk, tmWmn, tmDH, tmZmn, tmHmn, tmDW, j, eh, ew, s,
-                                              true);
+        e = launch_gemm<ProbDhPart, ProbDw, kPair>(10, dev, groups, tmZk, tmWmn, tmDH, tmZmn, tmHmn, tmDW, j, eh, ew, s);
       }
     }
     if (e != cudaSuccess) return KD_ERR_CUDA;
