@@ -686,16 +686,17 @@ __global__ void __launch_bounds__(kThreads, kResident) policy_one_kernel(const P
   if (blockIdx.x == 0) policy_join(A, gridDim.x, red);
 }
 
-// out = x g, the gradient of a loss whose unit gradient x was kept.
+// out = x g, the gradient of a loss whose unit gradient x was kept; 0 where x is 0
+// (a token that takes no part), also for a g that is not finite.  out may be x:
+// each value is read and written by one thread.
 template <bool VEC>
-__global__ void __launch_bounds__(kThreads) scale_kernel(const float* __restrict__ x, const float* __restrict__ g,
-                                                         float* __restrict__ out, int n) {
+__global__ void __launch_bounds__(kThreads) scale_kernel(const float* x, const float* __restrict__ g, float* out, int n) {
   const float s = *g;
   for (int64_t t0 = 4 * ((int64_t)blockIdx.x * kThreads + threadIdx.x); t0 < n; t0 += 4 * (int64_t)gridDim.x * kThreads) {
     float v[4];
     load4<VEC>(x, (int)t0, 0, n, v);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] *= s;
+    for (int j = 0; j < 4; ++j) v[j] = v[j] != 0.f ? v[j] * s : 0.f;
     store4<VEC>(out, (int)t0, 0, n, v);
   }
 }

@@ -391,9 +391,10 @@ int kd_policy_loss(const float* logp, const float* old_logp, const float* ref_lo
                    int per_sequence, const float* grad_loss, float* loss, float* dlogp,
                    void* workspace, size_t workspace_bytes, void* stream);
 
-/* out[i] = x[i] * *g (fp32 [N]): the gradient of a loss whose unit gradient
- * x one of the calls above has written, for an upstream gradient g on the
- * device.  out may be x. */
+/* out[i] = x[i] * *g (fp32 [N]), and 0 where x[i] is 0, also for a g that is
+ * infinite or NaN: the gradient of a loss whose unit gradient x one of the
+ * calls above has written, for an upstream gradient g on the device.  out may
+ * be x. */
 int kd_scale_gradient(const float* x, const float* g, float* out, int64_t N, void* stream);
 
 /* Failure-detection self-test.  Every pipeline wait in the kernels is
