@@ -232,6 +232,10 @@ __device__ __forceinline__ RowCoef row_coef(const RowScales& B, int n, float zy,
   const float L = g * om - h * (1.f - om) * (logp + ent);
   const bool own = fabsf(L) > base * 9.77e-4f;                 // 2^-10
   scale = own ? L : base;
+  if (scale == 0.f) {                          // g / T and h / T are below the smallest float
+    c.a = c.b = c.label = 0.f;
+    return c;
+  }
   c.a = -fmaf(h, ent, g) / scale;
   c.b = -h * kLn2 / scale;
   c.label = own ? 1.f : L / scale;
