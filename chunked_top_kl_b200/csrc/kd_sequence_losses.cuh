@@ -629,9 +629,18 @@ __device__ __forceinline__ void policy_losses(const PolicyArgs& A, int sum_block
                              on ? (A.adv_per_seq ? as : a[j]) : 0.f, l[j], k[j], c[j], d[j]);
             d[j] = on ? wg * m[j] * d[j] : 0.f;
           }
-          sum_l += w * (double)fmaf(m[0], l[0], fmaf(m[1], l[1], fmaf(m[2], l[2], m[3] * l[3])));
-          sum_k += w * (double)fmaf(m[0], k[0], fmaf(m[1], k[1], fmaf(m[2], k[2], m[3] * k[3])));
-          sum_c += w * (double)fmaf(m[0], c[0], fmaf(m[1], c[1], fmaf(m[2], c[2], m[3] * c[3])));
+          // in 64 bits, where the products are exact and terms that cancel leave what is left of them
+          double tl = 0.0, tk = 0.0, tc = 0.0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const double wide = (double)m[j];
+            tl = fma(wide, (double)l[j], tl);
+            if (KL != kNoKl) tk = fma(wide, (double)k[j], tk);
+            if (c[j] != 0.f) tc += wide;
+          }
+          sum_l += w * tl;
+          sum_k += w * tk;
+          sum_c += w * tc;
         }
       }
       if (A.dlogp) store4<VEC>(A.dlogp, t0, lo, hi, d);
