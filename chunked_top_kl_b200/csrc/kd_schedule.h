@@ -135,6 +135,9 @@ KD_HD Raster forward_raster(int64_t m_tiles, int64_t n_tiles, int grid, int64_t 
 // every CTA pair with a single band of rows.
 constexpr int kLogpMaxSplits = 96;
 
+// Ranges of a band of half the height, one CTA each (up to 128 tokens): one for every SM.
+constexpr int kSingleMaxSplits = 160;
+
 // Partial slots (one per row and column range) for N tokens: 16 ranges of
 // every row, as the distillation forward has, and 96 for up to one band of
 // rows, so that few live rows can be cut finer.

@@ -923,7 +923,6 @@ int logp_common(const void* H, const void* W, const void* labels, int labels_i64
 // longer hide) for the same bytes: 64 tokens at V = 201,088, d = 2880 250-260 us
 // in pairs, 209 us (5.5 TB/s) in single CTAs; V = 32,000, d = 2048 61 and 49 us.
 constexpr int64_t kSingleRows = 128;
-constexpr int kSingleMaxSplits = 160;       // column ranges of the one band: a range for every SM
 
 template <bool ENT>
 int logp_forward(const void* H, const void* W, int64_t N, int64_t d, int64_t V, float T, float* logp, float* kept,

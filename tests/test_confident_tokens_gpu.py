@@ -41,7 +41,7 @@ def _exact(H, y, T):
     return at, s / (1 + s), p, logp, ent, gap
 
 
-@pytest.mark.parametrize("N", [5, 8, 60, 300])
+@pytest.mark.parametrize("N", [5, 8, 12, 60, 300])
 @pytest.mark.parametrize("T", [1.0, 2.0])
 @pytest.mark.parametrize("entropy", [False, True])
 def test_forward(kd, N, T, entropy):                                         # noqa: F811
