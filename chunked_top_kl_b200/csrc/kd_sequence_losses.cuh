@@ -143,7 +143,7 @@ __device__ __forceinline__ double team_sum(double v, double* red) {
 // Calls body(team, item, lo, hi, thread in the team) for the block's items; every
 // thread of a team calls together.  Among short sequences one that is long is
 // left to the whole block: a warp would still be at it when all others are done
-// (32,768 tokens among 2,000 sequences of 150: policy loss 84 us, by warps alone
+// (32,768 tokens among 2,000 sequences of 150: policy loss 92 us, by warps alone
 // 480; 200,000 sequences of 100 tokens pay 3% for the question).
 constexpr int kWarpItemTokens = 2048;
 
@@ -408,11 +408,14 @@ __global__ void __launch_bounds__(kThreads, kResident) pref_one_kernel(const Pre
 // treats old, ref and A as constants.
 //
 // Whether a token is clipped is decided on the exact difference x, against
-// log(1 + hi), log(1 - lo) and log c, and not on a rounded exponential.  e^x and
-// the KL term are taken in 32 bits; e^-y - 1 + y, which cancels for small y, by
-// its series for |y| < 1/2.  Tokens are computed
-// without branches, masked ones on zeros: four at a time in flight instead of
-// one behind the other.
+// log(1 + hi), log(1 - lo) and log c, and not on a rounded exponential.  In one
+// launch, where the time is the host's, a token's terms are computed in 64 bits.
+// In two, e^x and the KL term are taken in 32 (so that r or e^-y is infinite
+// above 3.4e38); e^-y - 1 + y, which cancels for small y, by its series for
+// |y| < 1/2.  There tokens are computed without branches, masked ones on zeros:
+// four at a time in flight instead of one behind the other.  Sums are 64-bit in
+// both: adding four tokens in 32 bits first would take 70.1 us instead of 71.8
+// for 22 million padded tokens, and lose what terms that cancel leave.
 
 enum { kK1 = 0, kK2 = 1, kK3 = 2, kNoKl = 3 };
 
@@ -665,9 +668,9 @@ __global__ void __launch_bounds__(kThreads, 8) policy_sums_kernel(const PolicyAr
   policy_sums<TEAM, VEC>(A, red);
 }
 
-// Five blocks an SM, 48 registers a thread and some spills: 69.8 us against 77.0
-// with four, for 22 million padded tokens (7.2 million of them unmasked).  Six take
-// 68.9 there, but 253 against 248 for 20 million tokens in sequences of 100.
+// Five blocks an SM, 48 registers a thread and some spills: 71.8 us against 78.0
+// with four, for 22 million padded tokens (6.6 million of them unmasked).  Six take
+// 71.3 there, but 53.7 against 51.4 for three million tokens in sequences of 150.
 template <int TEAM, bool VEC, int KL>
 __global__ void __launch_bounds__(kThreads, 5) policy_loss_kernel(const PolicyArgs A, int sum_blocks) {
   __shared__ double red[kThreads / 32];

@@ -538,8 +538,8 @@ logp_merge_kernel(const float4* __restrict__ part, const LiveRows* __restrict__ 
 // (through the partials, one range per block) are joined.
 //
 // Measured against the GEMM's 128-row tiles (us): V = 201,088, d = 2880, up to
-// eight tokens 195, nine to sixteen 223 against 202; V = 32,000, d = 2048, 37, and
-// 45 against 50; V = 8,000, d = 512, 15 against 20.  So nine to sixteen tokens come
+// eight tokens 190, nine to sixteen 223 against 205; V = 32,000, d = 2048, 31, and
+// 35 against 43; V = 8,000, d = 512, 17 against 20.  So nine to sixteen tokens come
 // here where W is small (kFewWideBytes) and launches are a part of the time.
 //
 // Every kFewBatch k blocks the products start from zero and are added up in

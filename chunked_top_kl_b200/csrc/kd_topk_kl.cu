@@ -921,7 +921,7 @@ int logp_common(const void* H, const void* W, const void* labels, int labels_i64
 // Up to 128 tokens fill half of a CTA pair's 256-row tile: the forward product
 // then runs 128-row tiles of one CTA each, half the products (which W's bytes no
 // longer hide) for the same bytes: 64 tokens at V = 201,088, d = 2880 250-260 us
-// in pairs, 209 us (5.5 TB/s) in single CTAs; V = 32,000, d = 2048 61 and 49 us.
+// in pairs, 206 us (5.6 TB/s) in single CTAs; V = 32,000, d = 2048 61 and 43 us.
 constexpr int64_t kSingleRows = 128;
 
 template <bool ENT>
