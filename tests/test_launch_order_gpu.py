@@ -91,15 +91,17 @@ def test_followers_start_after_the_call(kd, follow):                         # n
     early = {}
     for name, call in _calls(kd).items():
         call()
-        torch.cuda.synchronize()
-        out = torch.zeros(2, dtype=torch.int64, device="cuda")
-        torch.cuda.synchronize()
-        keep = call()
-        assert follow(out.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
-        torch.cuda.synchronize()
-        del keep
-        started, over = out.tolist()
-        assert 0 < started <= over
-        if over - started > 20_000:                # ns; a wait that has nothing to wait for takes about one
-            early[name] = over - started
+        waits = []
+        for _ in range(3):
+            out = torch.zeros(2, dtype=torch.int64, device="cuda")
+            torch.cuda.synchronize()
+            keep = call()
+            assert follow(out.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
+            torch.cuda.synchronize()
+            del keep
+            started, over = out.tolist()
+            assert 0 < started <= over
+            waits.append(over - started)
+        if min(waits) > 20_000:                    # ns; a wait that has nothing to wait for takes about a thousand
+            early[name] = waits
     assert not early

@@ -37,16 +37,20 @@ def test_a_timeout_makes_the_gradients_nan(kd, chunk, dW_dtype, given):      # n
     dH, dW = call()
     assert kd.check(ws) == (_abi.KD_OK, 0) and bool(torch.isfinite(dH).all())
     assert dW is None or bool(torch.isfinite(dW).all())
-    torch.cuda.synchronize()
-    start.record()
-    dH, dW = call()
-    end.record()
-    time.sleep(0.002)                                         # the call has cleared the word
-    with torch.cuda.stream(side):
-        status[1:].copy_(one, non_blocking=True)
-        done.record()
-    torch.cuda.synchronize()
-    assert start.elapsed_time(done) < 0.8 * start.elapsed_time(end)       # ... and is still at its products
+    for _ in range(10):
+        torch.cuda.synchronize()
+        start.record()
+        dH, dW = call()
+        end.record()
+        time.sleep(0.002)                                     # the call, of 10 ms and more, has cleared the word
+        with torch.cuda.stream(side):
+            status[1:].copy_(one, non_blocking=True)
+            done.record()
+        torch.cuda.synchronize()
+        if start.elapsed_time(done) < 0.8 * start.elapsed_time(end):
+            break                                             # ... and was still at its products (no pause of the host)
+    else:
+        pytest.skip("the host never set the word in time")
     assert kd.check(ws)[0] == _abi.KD_ERR_TIMEOUT
     assert bool(torch.isnan(dH).all())
     assert dW is None or bool(torch.isnan(dW).all())
