@@ -169,7 +169,10 @@ def policy_loss_forward_backward(logp, old_logp, advantages, ref_logp=None, mask
     sequence.  ``reduce``: ``token`` divides the weighted sum by the mask's sum;
     ``sequence`` averages each sequence over its mask, then over all S
     sequences (an empty one counts 0).  kl and clip_fraction are averaged the
-    same way.  A packed ``logp`` without offsets is one sequence."""
+    same way.  A packed ``logp`` without offsets is one sequence.  Sums are in 64
+    bits; a token's terms are in 64 bits up to about a million tokens in 592
+    sequences (4,736 of a mean length up to 192) and in 32 above, where a ratio
+    or exp(-y) beyond 3.4e38 is infinite."""
     return _policy(logp, old_logp, advantages, ref_logp, mask, offsets, clip_low, clip_high, dual_clip, kl_coef, kl,
                    reduce, grad_loss, True)
 
